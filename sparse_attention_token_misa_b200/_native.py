@@ -24,6 +24,11 @@ OP_APPEND_KEYS = 6
 OP_SPARSE_MLA = 7
 OP_INDEX_DECODE = 8
 
+OP_APPEND_KV = 9
+OP_READ_KV = 10
+OP_SPARSE_MLA_Q = 11
+OP_PREFIX_MLA = 12
+
 DEVERR_TIMEOUT = 1
 DEVERR_BAD_SEQ = 2
 DEVERR_BAD_HEAD = 4
@@ -85,6 +90,18 @@ SIGNATURES = {
                                   c_int, c_int, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
 }
 
+# the same for include/misa_latent.h
+LATENT_SIGNATURES = {
+    "misa_kv_row_bytes": (c_i64, [c_int]),
+    "misa_append_kv": (c_int, [c_vp, c_i64, c_int, c_vp, c_vp, c_int, c_vp, c_i64, c_i64, c_vp, c_size, c_vp]),
+    "misa_read_kv": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_int, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp,
+                             c_vp, c_size, c_vp]),
+    "misa_sparse_mla_q": (c_int, [c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_int, c_int, c_vp, c_int, c_i64,
+                                  ctypes.c_float, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "misa_prefix_mla": (c_int, [c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, c_int, ctypes.c_float,
+                                c_vp, c_vp, c_vp, c_size, c_vp]),
+}
+
 
 class MisaError(RuntimeError):
     """A libmisa call returned a non-OK status."""
@@ -103,7 +120,7 @@ def lib() -> ctypes.CDLL:
                 f"libmisa.so not found at {LIB_PATH}; build it with "
                 "`python -m sparse_attention_token_misa_b200.build`")
         l = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **LATENT_SIGNATURES}.items():
             f = getattr(l, name)
             f.restype = res
             f.argtypes = args

@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "../../include/misa.h"
+#include "../../include/misa_latent.h"
 #include "launch.h"
 
 namespace {
@@ -127,6 +128,14 @@ size_t misa_workspace_bytes(int op, int T, int H, int64_t L, int B, int k, int k
     case MISA_OP_SPARSE_MLA:
       if (k < 1) return 0;
       return kErrBytes + static_cast<size_t>(T) * misa::sparse_mla_chunks(k) * H * (MISA_MLA_DV + 2) * sizeof(float);
+    case MISA_OP_APPEND_KV:
+    case MISA_OP_READ_KV:
+      return kErrBytes;
+    case MISA_OP_SPARSE_MLA_Q:
+      if (k < 1) return 0;
+      return kErrBytes + misa::latent_mla_scratch_bytes(T, H, k);
+    case MISA_OP_PREFIX_MLA:
+      return kErrBytes + misa::latent_mla_scratch_bytes(T, H, L);
     case MISA_OP_HISA_BLOCK_FILTER: {
       if (B < 1) return 0;
       const int64_t M = ceil_div(L, B);

@@ -111,6 +111,37 @@ cudaError_t launch_sparse_mla(const uint16_t* q, const uint16_t* kv, int64_t nse
                               float scale, uint16_t* out, float* lse, float* part_o, float* part_ml, uint32_t* err,
                               cudaStream_t stream);
 
+// The latent cache written and read back (kv_cache.cu).
+cudaError_t launch_append_kv(const uint16_t* rows, int64_t nseq, int n_new, const int32_t* counts, const int32_t* len,
+                             int fmt, void* cache, int64_t seq_stride, int64_t L_cap, uint32_t* err,
+                             cudaStream_t stream);
+cudaError_t launch_read_kv(const void* cache, int fmt, int64_t nseq, int64_t seq_stride, int64_t L,
+                           const int32_t* seq_of, int T, const int32_t* idx, int64_t idx_stride, const int32_t* first,
+                           const int32_t* prefix_len, int64_t n, uint16_t* out, uint32_t* err, cudaStream_t stream);
+
+// Attention over a latent cache (latent_mla.cu): listed rows (idx) or the
+// prefix (idx NULL).
+struct LatentArgs {
+  const uint16_t* q;
+  const void* cache;
+  int fmt;
+  int64_t nseq, seq_stride, L;
+  const int32_t* seq_of;
+  const int32_t* prefix_len;
+  const int32_t* idx;
+  int k;
+  int64_t idx_stride;
+  int T, Hq;
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  uint32_t* err;
+  void* scratch;
+};
+// Scratch behind the error word for T queries of Hq heads with at most n rows each.
+size_t latent_mla_scratch_bytes(int T, int Hq, int64_t n);
+cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream);
+
 cudaError_t launch_hisa_expand(const int32_t* blocks, const int32_t* prefix_len, int T, int m, int B, int S,
                                int64_t L, int32_t* cand, cudaStream_t stream);
 

@@ -1,0 +1,223 @@
+"""The latent key/value cache in 16, 8 or 4 bits and the attention that reads it.
+
+Bindings of include/misa_latent.h (argument marshalling only), and LatentCache,
+which keeps a cache, its lengths and the workspaces of one batch together.
+
+A cache is a tensor [nseq, L, row]: bf16 rows of 576 ("bf16"), or uint8 rows of
+656 ("mx8") or 400 bytes ("mx4").  The form is read off the tensor.
+"""
+from __future__ import annotations
+
+import contextlib
+import math
+
+import torch
+
+from . import _native as nat
+from ._native import MLA_DQK, MLA_DV, _call, _p, _req, _shape
+
+KV_FORMS = {"bf16": 0, "mx8": 1, "mx4": 2}       # MISA_KV_BF16, MISA_KV_MX8, MISA_KV_MX4
+_ROW_BYTES = {"bf16": 1152, "mx8": 656, "mx4": 400}
+
+
+def kv_row_bytes(form: str) -> int:
+    """Bytes of one cache row in this form."""
+    if form not in KV_FORMS:
+        raise ValueError(f"form must be one of {tuple(KV_FORMS)}")
+    return int(nat.lib().misa_kv_row_bytes(KV_FORMS[form]))
+
+
+def alloc_kv_cache(nseq: int, L: int, form: str, device=None) -> torch.Tensor:
+    """A cache of nseq sequences of L rows, zeroed (every row reads back as zeros)."""
+    kv_row_bytes(form)
+    if form == "bf16":
+        return torch.zeros((nseq, L, MLA_DQK), dtype=torch.bfloat16, device=device or "cuda")
+    return torch.zeros((nseq, L, _ROW_BYTES[form]), dtype=torch.uint8, device=device or "cuda")
+
+
+def _cache_form(cache: torch.Tensor) -> str:
+    if cache.dim() == 3:
+        for form, nbytes in _ROW_BYTES.items():
+            want = (torch.bfloat16, MLA_DQK) if form == "bf16" else (torch.uint8, nbytes)
+            if (cache.dtype, cache.shape[2]) == want:
+                if cache.stride(2) != 1 or cache.stride(1) != cache.shape[2]:
+                    raise ValueError("cache rows must be contiguous and follow one another")
+                return form
+    raise ValueError("cache: expected shape [nseq, L, 576] bf16 or [nseq, L, 656 or 400] uint8, got "
+                     f"{tuple(cache.shape)} {cache.dtype}")
+
+
+def _seq_stride(cache: torch.Tensor) -> int:
+    return int(cache.stride(0)) * cache.element_size() if cache.shape[0] > 1 else 0
+
+
+def _idx_stride(idx: torch.Tensor) -> int:
+    """Elements between the rows of idx (torch leaves any stride on a single row)."""
+    return int(idx.stride(0)) if idx.shape[0] > 1 else idx.shape[1]
+
+
+@contextlib.contextmanager
+def _on(first: torch.Tensor, stream, *others):
+    """The device of `first` made current (the library launches there; every
+    tensor has to be on it), and `stream`, so that what a call allocates for
+    itself belongs to the stream that uses it."""
+    _p(first)
+    for t in others:
+        if t is not None and (_p(t), t.device)[1] != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    with torch.cuda.device(first.device):
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=first.device)
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"tensors on {first.device}, stream on {stream.device}")
+        with torch.cuda.stream(stream):
+            yield torch.cuda.current_stream().cuda_stream
+
+
+def append_kv(cache: torch.Tensor, lens: torch.Tensor, rows: torch.Tensor, counts: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> None:
+    """misa_append_kv: rows [nseq, n_new, 576] bf16, the first counts[b] (None:
+    all) of each sequence, go to rows [lens[b], lens[b] + counts[b]) of cache,
+    quantised to its form.  lens is not advanced."""
+    form = _cache_form(cache)
+    _req(rows, torch.bfloat16, "rows")
+    _req(lens, torch.int32, "lens")
+    nseq, L_cap, _ = cache.shape
+    _shape(rows, "rows", nseq, None, MLA_DQK)
+    _shape(lens, "lens", nseq); _shape(counts, "counts", nseq)
+    if counts is not None:
+        _req(counts, torch.int32, "counts")
+    if rows.shape[1] == 0:
+        return
+    with _on(cache, stream, lens, rows, counts, workspace) as s:
+        ws = workspace if workspace is not None else nat.alloc_workspace(256, cache.device)
+        _call("misa_append_kv", _p(rows), nseq, rows.shape[1], _p(counts), _p(lens), KV_FORMS[form], _p(cache),
+              _seq_stride(cache), L_cap, _p(ws), ws.numel(), s)
+
+
+def read_kv(cache: torch.Tensor, seq_of: torch.Tensor, idx: torch.Tensor | None = None,
+            first: torch.Tensor | None = None, n: int | None = None, prefix_len: torch.Tensor | None = None,
+            out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """misa_read_kv -> [T, n, 576] bf16: the rows idx [T, n] (-1: zeros) of cache
+    seq_of[t], or n rows from first[t] (None: 0) on, zeros at and past prefix_len[t]
+    (None: the cache's length)."""
+    form = _cache_form(cache)
+    nseq, L, _ = cache.shape
+    _req(seq_of, torch.int32, "seq_of"); _shape(seq_of, "seq_of", None)
+    T = seq_of.shape[0]
+    if idx is not None:
+        if first is not None or prefix_len is not None or n is not None:
+            raise ValueError("idx goes without first, n and prefix_len")
+        _req(idx, torch.int32, "idx", contiguous=False); _shape(idx, "idx", T, None)
+        if idx.stride(1) != 1:
+            raise ValueError("idx rows must be contiguous")
+        n = idx.shape[1]
+    elif n is None:
+        raise ValueError("read_kv takes idx or n")
+    for name, t in (("first", first), ("prefix_len", prefix_len)):
+        if t is not None:
+            _req(t, torch.int32, name); _shape(t, name, T)
+    if out is not None:
+        _req(out, torch.bfloat16, "out"); _shape(out, "out", T, n, MLA_DQK)
+    with _on(cache, stream, seq_of, idx, first, prefix_len, out, workspace) as s:
+        if out is None:
+            out = torch.empty((T, n, MLA_DQK), dtype=torch.bfloat16, device=cache.device)
+        ws = workspace if workspace is not None else nat.alloc_workspace(256, cache.device)
+        _call("misa_read_kv", _p(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _p(seq_of), T, _p(idx),
+              _idx_stride(idx) if idx is not None else 0, _p(first), _p(prefix_len), n, _p(out), _p(ws),
+              ws.numel(), s)
+    return out
+
+
+def _attend(op: int, q, cache, seq_of, per_query, scale, out, lse, want_lse, workspace, stream):
+    """Shared marshalling of the two attention calls; per_query is idx or prefix_len."""
+    form = _cache_form(cache)
+    sparse = op == nat.OP_SPARSE_MLA_Q
+    if sparse and form == "bf16":
+        raise ValueError("sparse_mla_q reads a quantised cache; sparse_mla reads bf16 rows")
+    if not (math.isfinite(scale) and scale >= 0):
+        raise ValueError("scale must be finite and not negative")
+    _req(q, torch.bfloat16, "q"); _req(seq_of, torch.int32, "seq_of")
+    _shape(q, "q", None, None, MLA_DQK)
+    T, Hq, _ = q.shape
+    nseq, L, _ = cache.shape
+    _shape(seq_of, "seq_of", T)
+    if out is not None:
+        _req(out, torch.bfloat16, "out"); _shape(out, "out", T, Hq, MLA_DV)
+    if lse is not None:
+        _req(lse, torch.float32, "lse"); _shape(lse, "lse", T, Hq)
+    with _on(q, stream, cache, seq_of, per_query, out, lse, workspace) as s:
+        if out is None:
+            out = torch.empty((T, Hq, MLA_DV), dtype=torch.bfloat16, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        ws = workspace
+        if ws is None:
+            k = per_query.shape[1] if sparse else 0
+            ws = nat.alloc_workspace(nat.workspace_bytes(op, T, Hq, L, 0, k), q.device)
+        head = (_p(q), _p(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _p(seq_of))
+        tail = (float(scale), _p(out), _p(lse), _p(ws), ws.numel(), s)
+        if sparse:
+            _call("misa_sparse_mla_q", *head, T, Hq, _p(per_query), per_query.shape[1], _idx_stride(per_query), *tail)
+        else:
+            _call("misa_prefix_mla", *head, _p(per_query), T, Hq, *tail)
+    return out, lse
+
+
+def sparse_mla_q(q, cache, seq_of, idx, scale: float, out=None, lse=None, want_lse: bool = False, workspace=None,
+                 stream=None):
+    """misa_sparse_mla_q -> (out [T, Hq, 512] bf16, lse [T, Hq] fp32 or None): q [T,
+    Hq, 576] bf16 over the rows idx [T, k] int32 (-1 = empty) of a quantised cache."""
+    _req(idx, torch.int32, "idx", contiguous=False)
+    _shape(idx, "idx", q.shape[0], None)
+    if idx.stride(1) != 1:
+        raise ValueError("idx rows must be contiguous")
+    return _attend(nat.OP_SPARSE_MLA_Q, q, cache, seq_of, idx, scale, out, lse, want_lse, workspace, stream)
+
+
+def prefix_mla(q, cache, seq_of, prefix_len, scale: float, out=None, lse=None, want_lse: bool = False,
+               workspace=None, stream=None):
+    """misa_prefix_mla -> (out [T, Hq, 512] bf16, lse [T, Hq] fp32 or None): q [T,
+    Hq, 576] bf16 over the rows below prefix_len [T] int32 of a cache in any form."""
+    _req(prefix_len, torch.int32, "prefix_len")
+    _shape(prefix_len, "prefix_len", q.shape[0])
+    return _attend(nat.OP_PREFIX_MLA, q, cache, seq_of, prefix_len, scale, out, lse, want_lse, workspace, stream)
+
+
+class LatentCache:
+    """The latent caches of nseq sequences with their lengths, and the buffers of
+    one batch of T queries: append and attend allocate nothing and can be
+    captured in a CUDA graph (lens advances on the device)."""
+
+    def __init__(self, nseq: int, L: int, form: str, T: int, Hq: int, k: int, device="cuda"):
+        self.nseq, self.L, self.form, self.T, self.Hq, self.k = nseq, L, form, T, Hq, k
+        self.rows = alloc_kv_cache(nseq, L, form, device)
+        self.lens = torch.zeros(nseq, dtype=torch.int32, device=device)
+        self.out = torch.empty((T, Hq, MLA_DV), dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+        self.ws = nat.alloc_workspace(256, device)
+        op = nat.OP_SPARSE_MLA if form == "bf16" else nat.OP_SPARSE_MLA_Q
+        self.ws_sparse = nat.alloc_workspace(nat.workspace_bytes(op, T, Hq, L, 0, k), device)
+        self.ws_prefix = nat.alloc_workspace(nat.workspace_bytes(nat.OP_PREFIX_MLA, T, Hq, L, 0), device)
+
+    def append(self, rows: torch.Tensor, counts: torch.Tensor | None = None) -> None:
+        """Write new rows behind each sequence's last one and advance its length.  A
+        sequence whose rows no longer fit (or whose count is out of range) is left
+        as it was, as misa_append_kv skips it and records it in `ws`."""
+        append_kv(self.rows, self.lens, rows, counts=counts, workspace=self.ws)
+        n = rows.shape[1]
+        new = self.lens + (n if counts is None else counts)
+        fits = (new <= self.L) if counts is None else (new <= self.L) & (counts >= 0) & (counts <= n)
+        self.lens.copy_(torch.where(fits, new, self.lens))
+
+    def attend(self, q, seq_of, idx, scale: float):
+        """Over the tokens the indexer lists -> (out, lse)."""
+        if self.form == "bf16":
+            return nat.sparse_mla(q, self.rows, seq_of, idx, scale, out=self.out, lse=self.lse,
+                                  workspace=self.ws_sparse)
+        return sparse_mla_q(q, self.rows, seq_of, idx, scale, out=self.out, lse=self.lse, workspace=self.ws_sparse)
+
+    def attend_prefix(self, q, seq_of, prefix_len, scale: float):
+        """Over the whole prefix -> (out, lse)."""
+        return prefix_mla(q, self.rows, seq_of, prefix_len, scale, out=self.out, lse=self.lse,
+                          workspace=self.ws_prefix)
