@@ -96,11 +96,10 @@ MISA_API misa_status misa_read_kv(const void* cache, int fmt, int64_t nseq, int6
  *   counts twice.  out: [T][Hq][512] bf16.  lse: [T][Hq] fp32, may be NULL.
  * A query with no valid slot, or with seq_of[t] outside [0, nseq) (which sets
  *   MISA_DEVERR_BAD_SEQ), gets zeros and lse = -inf.
- * Precision: products of bf16 numbers summed in fp32; weights rounded to bf16 for
- *   the value product and summed as rounded for the quotient, summed in fp32
- *   before rounding for lse; one rounding to bf16 at the end.
+ * Precision: products of bf16 numbers summed in fp32; weights summed in fp32 and
+ *   rounded to bf16 for the value product; one rounding to bf16 at the end.
  * Limits: 1 <= Hq <= 128, 1 <= k <= MISA_MAX_TOPK, T, L, nseq >= 1, L < 2^31,
- *   T * Hq < 2^31; scale finite and >= 0; q, cache, out 16-byte aligned;
+ *   T * Hq < 2^31, T < 2^29; scale finite and >= 0; q, cache, out 16-byte aligned;
  *   cache_seq_stride as misa_read_kv; fmt MISA_KV_MX8 or MISA_KV_MX4
  *   (misa_sparse_mla reads bf16 rows).
  * workspace: >= misa_workspace_bytes(MISA_OP_SPARSE_MLA_Q, T, Hq, 0, 0, k, 0).

@@ -35,7 +35,8 @@ misa_status attend(misa::LatentArgs& a, int64_t n, float scale, void* ws, size_t
   misa_status st = check_cache(a.cache, a.fmt, a.nseq, a.seq_stride, a.L);
   if (st != MISA_OK) return st;
   if (!aligned16(a.q) || !aligned16(a.out)) return MISA_ERR_INVALID_ARG;
-  if (a.Hq > MISA_MAX_HEADS || static_cast<int64_t>(a.T) * a.Hq >= kMax31) return MISA_ERR_UNSUPPORTED;
+  if (a.Hq > MISA_MAX_HEADS || static_cast<int64_t>(a.T) * a.Hq >= kMax31 || a.T >= (1 << 29))
+    return MISA_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, kErrBytes + misa::latent_mla_scratch_bytes(a.T, a.Hq, n));
   if (st != MISA_OK) return st;
   a.scale_log2 = scale * 1.4426950408889634f;
