@@ -137,9 +137,7 @@ __global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadParams p) {
       uint2 c;
       if (kFmt == MISA_KV_MX8) c = *reinterpret_cast<const uint2*>(src + piece * 8);
       else c = make_uint2(*reinterpret_cast<const uint32_t*>(src + piece * 4), 0u);
-      uint32_t second;
-      const uint32_t scale = kv_scale<kFmt>(src[kv_code_bytes(kFmt) + (piece >> 2)], &second);
-      y = kv_decode8<kFmt>(c.x, c.y, scale, second);
+      y = kv_decode8<kFmt>(c.x, c.y, kv_scale(src[kv_code_bytes(kFmt) + (piece >> 2)]));
     }
   }
   __stcs(reinterpret_cast<uint4*>(p.out) + g, y);

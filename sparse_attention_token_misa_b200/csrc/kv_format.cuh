@@ -4,9 +4,12 @@
 // An e4m3 (e2m1) number, its bits moved to the top of bf16's exponent and
 // mantissa fields, is that number times 2^-120 (2^-126): the fields line up, the
 // exponents differ by the two biases, and subnormal numbers stay right because
-// both fields are read the same way.  One bf16 product with a power of two then
-// gives element * 2^e, exactly: at most 4 significant bits, and an exponent that
-// the writer's range of e keeps among the normal bf16 numbers.
+// both fields are read the same way.  A bf16 product with 2^120 (2^126) gives the
+// element and one with its scale element * 2^e, both exactly: at most 4
+// significant bits, and an exponent that the writer's range of e keeps among the
+// normal bf16 numbers.  A scale byte is itself the exponent field of its power of
+// two: byte 255 is infinity, and its group's zeros become NaN; byte 0, which is
+// never written, is 0.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -36,47 +39,39 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t bf16x2_of(uint32_t bits) { return bits | (bits << 16); }
-
-// What scale byte b multiplies the moved bits by: 2^(b - 127 + shift), shift =
-// 120 or 126, as one factor while that is a bf16 number and as two behind it
-// (`second`, else 0).  Byte 255 is NaN.
-template <int kFmt>
-__device__ __forceinline__ uint32_t kv_scale(uint32_t b, uint32_t* second) {
-  constexpr uint32_t kShift = kFmt == MISA_KV_MX8 ? 120u : 126u;
-  *second = 0u;
-  if (b + kShift <= 254u) return bf16x2_of((b + kShift) << 7);
-  if (b == 255u) return bf16x2_of(0x7FC0u);
-  *second = bf16x2_of((b + kShift - 127u) << 7);
-  return bf16x2_of(254u << 7);
+template <uint32_t kSelect>   // bytes of a (0-3) and b (4-7) by nibble; 8 + i: the sign of byte i, eight times
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "n"(kSelect));
+  return d;
 }
 
-// Two entries of the pair of bytes (MX8) or of byte (MX4) `kPair` of w, moved to bf16 fields.
+// 2^(b - 127) twice.
+__device__ __forceinline__ uint32_t kv_scale(uint32_t b) { return b * 0x00800080u; }
+
+// Two entries as elements in bf16.  The element bytes go to the upper bytes of
+// the two halves, the first one's sign between them; one arithmetic shift moves
+// both, with the signs copied into the bits that the mask then clears.
 template <int kPair>
-__device__ __forceinline__ uint32_t moved_mx8(uint32_t w) {   // bytes 2 kPair, 2 kPair + 1
-  const uint32_t x = __byte_perm(w, 0u, kPair ? 0x3424 : 0x1404);
-  return (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+__device__ __forceinline__ uint32_t element2_mx8(uint32_t w) {   // bytes 2 kPair, 2 kPair + 1
+  const uint32_t x = kPair ? prmt<0x3A20>(w, 0u) : prmt<0x1800>(w, 0u);
+  return mul_bf16x2((static_cast<int32_t>(x) >> 4) & 0x87F087F0u, 0x7B807B80u);
 }
 template <int kPair>
-__device__ __forceinline__ uint32_t moved_mx4(uint32_t low, uint32_t w) {   // low = w << 4
-  const uint32_t x = __byte_perm(low, w, 0x4000 | (kPair << 12) | (kPair << 4));   // bytes 1 and 3: the even and odd entry
-  return (x & 0x80008000u) | ((x >> 6) & 0x01C001C0u);
+__device__ __forceinline__ uint32_t element2_mx4(uint32_t low, uint32_t w) {   // byte kPair; low = w << 4
+  const uint32_t x = prmt<0x4800 | (kPair << 12) | (kPair << 8) | (kPair << 4)>(low, w);
+  return mul_bf16x2((static_cast<int32_t>(x) >> 6) & 0x81C081C0u, 0x7E807E80u);
 }
 
-// Eight consecutive entries as bf16: codes in w0 (and w1 for MX8).
+// Eight consecutive entries as bf16: codes in w0 (and w1 for MX8), scale = kv_scale.
 template <int kFmt>
-__device__ __forceinline__ uint4 kv_decode8(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t second) {
-  uint4 y;
-  if (kFmt == MISA_KV_MX8) {
-    y = make_uint4(moved_mx8<0>(w0), moved_mx8<1>(w0), moved_mx8<0>(w1), moved_mx8<1>(w1));
-  } else {
-    const uint32_t low = w0 << 4;
-    y = make_uint4(moved_mx4<0>(low, w0), moved_mx4<1>(low, w0), moved_mx4<2>(low, w0), moved_mx4<3>(low, w0));
-  }
-  y = make_uint4(mul_bf16x2(y.x, scale), mul_bf16x2(y.y, scale), mul_bf16x2(y.z, scale), mul_bf16x2(y.w, scale));
-  if (second)
-    y = make_uint4(mul_bf16x2(y.x, second), mul_bf16x2(y.y, second), mul_bf16x2(y.z, second), mul_bf16x2(y.w, second));
-  return y;
+__device__ __forceinline__ uint4 kv_decode8(uint32_t w0, uint32_t w1, uint32_t scale) {
+  if (kFmt == MISA_KV_MX8)
+    return make_uint4(mul_bf16x2(element2_mx8<0>(w0), scale), mul_bf16x2(element2_mx8<1>(w0), scale),
+                      mul_bf16x2(element2_mx8<0>(w1), scale), mul_bf16x2(element2_mx8<1>(w1), scale));
+  const uint32_t low = w0 << 4;
+  return make_uint4(mul_bf16x2(element2_mx4<0>(low, w0), scale), mul_bf16x2(element2_mx4<1>(low, w0), scale),
+                    mul_bf16x2(element2_mx4<2>(low, w0), scale), mul_bf16x2(element2_mx4<3>(low, w0), scale));
 }
 
 // Scale byte of a group whose largest |entry| has these bf16 bits (sign clear):

@@ -75,41 +75,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// Arrive on the first CTA's barrier.
+// Arrive on the first CTA's barrier.  The release is the CTA's: what this warp
+// wrote is its own CTA's shared memory, which its own SM's tensor core reads, and
+// fence.proxy.async has ordered that.  (A release of the cluster's scope would wait
+// for the loads of the next unit and for a round trip to L2, about 1000 cycles.)
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait for barriers that the other CTA arrives on.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* err, volatile uint32_t* abort) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      record_error(err, MISA_DEVERR_TIMEOUT);
-      *abort = 1u;
-      return false;
-    }
-  }
-}
-// The same for a whole warp: one outcome for all lanes.
+// A wait of a whole warp: one outcome for all lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err, volatile uint32_t* abort) {
-  return __all_sync(0xffffffffu, wait_cluster(bar, parity, err, abort));
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort));
 }
 __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -157,9 +135,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
+__device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- rows
 // The work of a cluster: query t, tiles [tile0, tile1) of its n row slots.
@@ -178,26 +154,14 @@ __device__ __forceinline__ int32_t row_of(const Work& w, int s) {
   return id >= 0 && id < w.L ? id : -1;
 }
 
-// One 16-byte piece (8 entries) of a row as it is loaded: 8 or 4 bytes of codes,
-// or 16 bytes of rotary entries.
-template <int kFmt>
-struct Raw {
-  using Code = typename std::conditional<kFmt == MISA_KV_MX8, uint2, uint32_t>::type;
-};
-template <int kFmt>
-__device__ __forceinline__ uint4 widen(uint2 c, uint32_t scale_byte) {
-  uint32_t second;
-  const uint32_t scale = kv_scale<kFmt>(scale_byte, &second);
-  return kv_decode8<kFmt>(c.x, c.y, scale, second);
-}
 template <int kFmt>
 __device__ __forceinline__ uint2 load_code(const uint8_t* row, int entry) {   // 8 entries from `entry` on
   if (kFmt == MISA_KV_MX8) return __ldg(reinterpret_cast<const uint2*>(row + entry));
   return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row + entry / 2)), 0u);
 }
 
-// Signals a unit: this lane's writes are visible to the tensor cores, and the
-// warp arrives once.
+// Signals a unit: this lane's writes are visible to the tensor core, and the warp
+// arrives once.
 __device__ __forceinline__ void unit_ready(uint64_t* bar) {
   fence_proxy_async_smem();
   __syncwarp();
@@ -213,10 +177,15 @@ __device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid
   uint8_t* dst0 = sK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 16 apart: the same swizzle
   const int own = static_cast<int>(rank) * 64;
   auto prefetch = [&](int tile) {
-    if (tid < 64 && tile < w.tile1) {
-      const int32_t id = row_of(w, tile * kTile + own + tid);
-      if (id >= 0) l2_prefetch(w.base + static_cast<int64_t>(id) * kRow, kRow);
-    }
+    // (lines of 128 bytes, two threads a row; one bulk prefetch a row is issued lane
+    // by lane and took a warp 3000 cycles a tile)
+    if (tile >= w.tile1) return;
+    const int32_t id = row_of(w, tile * kTile + own + (tid >> 1));
+    if (id < 0) return;
+    const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow;
+#pragma unroll
+    for (int o = 0; o < kRow; o += 256)
+      if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o + (tid & 1) * 128);
   };
   prefetch(w.tile0);
   prefetch(w.tile0 + 1);
@@ -236,7 +205,7 @@ __device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid
 #pragma unroll
       for (int i = 0; i < 4; ++i) src[i] = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow + piece * 16;
       for (int g = 0; g < kKUnits; ++g) {
-        if (pending >= 0 && !__all_sync(0xffffffffu, try_wait_cluster(&empty[g], ph ^ 1u))) {
+        if (pending >= 0 && !__all_sync(0xffffffffu, mbar_try_wait(&empty[g], ph ^ 1u))) {
           cp_async_wait_group<0>();
           unit_ready(&full[pending]);
           pending = -1;
@@ -260,42 +229,55 @@ __device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid
     cp_async_wait_group<0>();
     if (pending >= 0) unit_ready(&full[pending]);
   } else {
+    // Absent rows: any row's codes with scales of zero, and no rotary entries.
     uint2 cur[kKUnitBlocks * 4];    // codes of the unit at hand (the rotary block apart)
     uint4 rope[4], scales[4];
-    auto load_unit = [&](int g, uint2* c) {   // of the rows `ids`
+    bool absent[4];
+    const uint8_t* src[4];
+    auto point = [&] {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) src[i] = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow;
+    };
+    auto load_unit = [&](int g, uint2* c) {
 #pragma unroll
       for (int bb = 0; bb < kKUnitBlocks; ++bb) {
         const int b = g * kKUnitBlocks + bb;
         if (b == kBlocks - 1) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          c[bb * 4 + i] = ids[i] >= 0 ? load_code<kFmt>(w.base + static_cast<int64_t>(ids[i]) * kRow, b * 64 + piece * 8)
-                                      : make_uint2(0u, 0u);
+        for (int i = 0; i < 4; ++i) c[bb * 4 + i] = load_code<kFmt>(src[i], b * 64 + piece * 8);
       }
     };
+    auto load_rest = [&] {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        scales[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_code_bytes(kFmt)));
+        rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
+        absent[i] = ids[i] < 0;
+      }
+    };
+    point();
     load_unit(0, cur);
+    load_rest();
+    load_ids(w.tile0 + 1);
+    const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
     uint32_t ph = 0;
     for (int tile = w.tile0; tile < w.tile1; ++tile, ph ^= 1u) {
       prefetch(tile + 2);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        scales[i] = rope[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (ids[i] >= 0) {
-          const uint8_t* row = w.base + static_cast<int64_t>(ids[i]) * kRow;
-          scales[i] = __ldg(reinterpret_cast<const uint4*>(row + kv_code_bytes(kFmt)));
-          rope[i] = __ldg(reinterpret_cast<const uint4*>(row + kv_rope_offset(kFmt) + piece * 16));
-        }
-      }
 #pragma unroll
       for (int g = 0; g < kKUnits; ++g) {
         uint2 nxt[kKUnitBlocks * 4];
         if (g + 1 < kKUnits) {
           load_unit(g + 1, nxt);
         } else {
-          load_ids(tile + 1);
+          point();
           load_unit(0, nxt);
         }
         if (!wait_warp(&empty[g], ph ^ 1u, err, abort)) return;
+        if (g == 0) {   // (here, not where they are loaded: this waits for them)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (absent[i]) scales[i] = rope[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
         for (int bb = 0; bb < kKUnitBlocks; ++bb) {
           const int b = g * kKUnitBlocks + bb;
@@ -306,7 +288,8 @@ __device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid
               y = rope[i];
             } else {
               const uint32_t sw = b < 2 ? scales[i].x : b < 4 ? scales[i].y : b < 6 ? scales[i].z : scales[i].w;
-              y = widen<kFmt>(cur[bb * 4 + i], (sw >> (8 * ((b & 1) * 2 + (piece >> 2)))) & 255u);
+              const uint2 c = cur[bb * 4 + i];
+              y = kv_decode8<kFmt>(c.x, c.y, kv_scale(__byte_perm(sw, 0u, sel + (b & 1) * 2)));
             }
             *reinterpret_cast<uint4*>(dst0 + b * kBlockBytes + i * 2048) = y;
           }
@@ -315,6 +298,8 @@ __device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid
 #pragma unroll
         for (int j = 0; j < kKUnitBlocks * 4; ++j) cur[j] = nxt[j];
       }
+      load_rest();                // of the rows `src` points at now
+      load_ids(tile + 2);
     }
   }
 }
@@ -339,7 +324,7 @@ __device__ __forceinline__ void bring_values(const Work& w, uint32_t rank, int t
     uint32_t ph = 0;
     for (int tile = w.tile0; tile < w.tile1; ++tile, ph ^= 1u) {
       for (int g = 0; g < kVUnits; ++g) {
-        if (pending >= 0 && !__all_sync(0xffffffffu, try_wait_cluster(&empty[g], ph ^ 1u))) {
+        if (pending >= 0 && !__all_sync(0xffffffffu, mbar_try_wait(&empty[g], ph ^ 1u))) {
           cp_async_wait_group<0>();
           unit_ready(&full[pending]);
           pending = -1;
@@ -365,40 +350,46 @@ __device__ __forceinline__ void bring_values(const Work& w, uint32_t rank, int t
     if (pending >= 0) unit_ready(&full[pending]);
   } else {
     uint2 cur[8], scales[2];
-    auto load_unit = [&](uint2* c, uint2* s) {
+    const uint8_t* src[2];
+    bool absent[2];
+    auto load_unit = [&](uint2* c, uint2* s) {   // of the rows `ids`
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint8_t* row = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow;
-        s[i] = ids[i] >= 0 ? __ldg(reinterpret_cast<const uint2*>(row + kv_code_bytes(kFmt) + rank * 8)) : make_uint2(0u, 0u);
+        src[i] = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow;
+        s[i] = __ldg(reinterpret_cast<const uint2*>(src[i] + kv_code_bytes(kFmt) + rank * 8));
+        absent[i] = ids[i] < 0;
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
-          c[i * 4 + a] = ids[i] >= 0 ? load_code<kFmt>(row, static_cast<int>(rank) * 256 + a * 64 + piece * 8)
-                                     : make_uint2(0u, 0u);
+        for (int a = 0; a < 4; ++a) c[i * 4 + a] = load_code<kFmt>(src[i], static_cast<int>(rank) * 256 + a * 64 + piece * 8);
       }
     };
     load_unit(cur, scales);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (absent[i]) scales[i] = make_uint2(0u, 0u);
+    load_ids(w.tile0, 1);
+    const uint32_t sel = 0x4440u | (piece >> 2);
     uint32_t ph = 0;
     for (int tile = w.tile0; tile < w.tile1; ++tile, ph ^= 1u) {
 #pragma unroll
       for (int g = 0; g < kVUnits; ++g) {
         uint2 nxt[8], nscales[2];
-        if (g + 1 < kVUnits) load_ids(tile, g + 1);
-        else load_ids(tile + 1, 0);
         load_unit(nxt, nscales);
+        if (g + 2 < kVUnits) load_ids(tile, g + 2);
+        else load_ids(tile + 1, g + 2 - kVUnits);
         if (!wait_warp(&empty[g], ph ^ 1u, err, abort)) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
-            const uint32_t sw = a < 2 ? scales[i].x : scales[i].y;
+            const uint2 c = cur[i * 4 + a];
             *reinterpret_cast<uint4*>(dst0 + g * kVUnitBytes + a * kVAtom + i * 2048) =
-                widen<kFmt>(cur[i * 4 + a], (sw >> (8 * ((a & 1) * 2 + (piece >> 2)))) & 255u);
+                kv_decode8<kFmt>(c.x, c.y, kv_scale(__byte_perm(a < 2 ? scales[i].x : scales[i].y, 0u, sel + (a & 1) * 2)));
           }
         unit_ready(&full[g]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
-        scales[0] = nscales[0];
-        scales[1] = nscales[1];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) scales[i] = absent[i] ? make_uint2(0u, 0u) : nscales[i];
       }
     }
   }
@@ -418,8 +409,8 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *sQ = smem + kOffQ, *sK = smem + kOffK, *sV = smem + kOffV, *sP = smem + kOffP;
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + kOffBar);   // first CTA: unit brought by both
-  uint64_t* kempty = kfull + kKUnits;                              // unit multiplied
-  uint64_t* vfull = kempty + kKUnits;
+  uint64_t* kempty = kfull + kKUnits;    // unit multiplied
+  uint64_t* vfull = kempty + kKUnits;    // first CTA
   uint64_t* vempty = vfull + kVUnits;
   uint64_t* sfull = vempty + kVUnits;    // [2] S complete
   uint64_t* sempty = sfull + 2;          // [2] first CTA: S read by both
@@ -501,13 +492,12 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
       const bool landed = mbar_wait(qfull, 0, err, abort);
       if (landed) arrive_leader(qready);
       if (rank == 0) {
-        bool ok = landed && wait_cluster(qready, 0, err, abort);
         const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK), va = smem_u32(sV), pa = smem_u32(sP);
         auto scores = [&](int i) {   // S of tile i (counted from the cluster's first)
-          if (!wait_cluster(&sempty[i & 1], ((i >> 1) & 1) ^ 1u, err, abort)) return false;
+          if (!mbar_wait(&sempty[i & 1], ((i >> 1) & 1) ^ 1u, err, abort)) return false;
           const uint32_t d = tmem + kTmemS + (i & 1) * 64;
           for (int g = 0; g < kKUnits; ++g) {
-            if (!wait_cluster(&kfull[g], i & 1, err, abort)) return false;
+            if (!mbar_wait(&kfull[g], i & 1, err, abort)) return false;
             tc_fence_after();
 #pragma unroll
             for (int bb = 0; bb < kKUnitBlocks; ++bb)
@@ -522,9 +512,9 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
           return true;
         };
         auto values = [&](int i) {
-          if (!wait_cluster(pfull, i & 1, err, abort)) return false;
+          if (!mbar_wait(pfull, i & 1, err, abort)) return false;
           for (int g = 0; g < kVUnits; ++g) {
-            if (!wait_cluster(&vfull[g], i & 1, err, abort)) return false;
+            if (!mbar_wait(&vfull[g], i & 1, err, abort)) return false;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
@@ -540,14 +530,14 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
           commit_pair(pvdone);
           return true;
         };
-        ok = ok && scores(0);
+        bool ok = landed && mbar_wait(qready, 0, err, abort) && scores(0);
         for (int i = 0; i < ntiles && ok; ++i) {
           if (i + 1 < ntiles) ok = scores(i + 1);
           ok = ok && values(i);
         }
         commit_pair(done);
       }
-      wait_cluster(done, 0, err, abort);   // both: nothing reads this CTA's memory any more
+      mbar_wait(done, 0, err, nullptr);   // both: nothing reads this CTA's memory any more
     }
     __syncwarp();
   } else {
