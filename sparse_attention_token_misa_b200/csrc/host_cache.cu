@@ -81,6 +81,21 @@ bool encode_2d_map(CUtensorMap* map, bool bf16, const void* base, uint64_t inner
   return r == CUDA_SUCCESS;
 }
 
+bool encode_3d_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t seqs, uint64_t row_bytes,
+                   uint64_t seq_bytes, uint32_t box_inner, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  std::memset(map, 0, sizeof(*map));
+  cuuint64_t dims[3] = {inner, rows, seqs};
+  cuuint64_t strides[2] = {row_bytes, seq_bytes};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 int occupancy_blocks(const void* func, int threads, size_t smem) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;

@@ -37,6 +37,9 @@ misa_status attend(misa::LatentArgs& a, int64_t n, float scale, void* ws, size_t
   if (!aligned16(a.q) || !aligned16(a.out)) return MISA_ERR_INVALID_ARG;
   if (a.Hq > MISA_MAX_HEADS || static_cast<int64_t>(a.T) * a.Hq >= kMax31 || a.T >= (1 << 29))
     return MISA_ERR_UNSUPPORTED;
+  // a TMA map reads bf16 rows: its strides are 40 bits
+  if (a.fmt == MISA_KV_BF16 && (a.seq_stride >> 40 || (a.L * misa::kv_row_bytes(MISA_KV_BF16)) >> 40))
+    return MISA_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, kErrBytes + misa::latent_mla_scratch_bytes(a.T, a.Hq, n));
   if (st != MISA_OK) return st;
   a.scale_log2 = scale * 1.4426950408889634f;

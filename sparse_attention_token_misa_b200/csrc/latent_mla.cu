@@ -14,25 +14,33 @@
 //
 // Rows come in tiles of 128.  Per tile:
 //  1. S = Q K^T: CTA u holds rows [64 u, 64 u + 64) of the tile, all 576 entries,
-//     in 9 blocks of 64 (3 units of 3 blocks in a ring).  S in TMEM: lane l < 64
-//     has head l against rows 0..63, lane 64 + l the same head against 64..127.
+//     in 9 blocks of 64.  S in TMEM: lane l < 64 has head l against rows 0..63,
+//     lane 64 + l the same head against rows 64..127.
 //  2. Softmax in one pass with a running reference m: when a tile's maximum is
 //     more than 2^8 above 2^m, the sums so far are scaled and m moves (p stays
 //     below 2^8, exact enough in bf16 and fp32).  p goes to shared memory as bf16.
-//  3. O += P V: CTA u brings entries [256 u, 256 u + 256) of all 128 rows, as units
-//     of 32 rows in a ring (rows of 64 entries in 128-byte swizzled atoms, read
-//     MN-major, so nothing is transposed).  O stays in TMEM, 256 columns.
+//  3. O += P V: CTA u brings entries [256 u, 256 u + 256) of all 128 rows, 32 rows at
+//     a time (rows of 64 entries in 128-byte swizzled atoms, read MN-major, so
+//     nothing is transposed).  O stays in TMEM, 256 columns.
 // S has two places, so that the products of tile i + 1 run while the softmax of
 // tile i does.  Quantised rows become bf16 (exactly) on the way from global to
-// shared memory, in registers; bf16 rows are copied asynchronously.  Rows two
-// tiles ahead are asked into L2.
+// shared memory, in registers, the next unit's codes in flight behind; bf16 rows
+// come by TMA.
+//
+// What bounds a tile: shared memory, 128 bytes a cycle.  Rows written 139 KB, read
+// 147 KB (S) and 98 KB (O), P 16 KB twice: about 3200 cycles, where the products
+// take 2176 of the tensor cores.  Half of the values are in the other operand
+// already; copying them there, shared memory to shared memory, instead of bringing
+// them twice was slower (3800 cycles a tile for the copies alone).
 //
 // Few queries: the rows of each are split over several clusters, whose partial
 // sums a second kernel joins in a fixed order.
 //
 // Roles (416 threads a CTA): warps 0-3 softmax and output (a lane of TMEM each),
 // warp 4 TMEM and, in the first CTA, the MMAs, warps 5-8 bring the rows of S,
-// warps 9-12 those of O.  Waits are bounded.
+// warps 9-12 those of O.  Shared memory is addressed from one 32-bit base: with a
+// pointer a barrier the kernel spilled, and what shared memory leaves of L1 does
+// not hold the stack.  Waits are bounded.
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"
@@ -45,26 +53,112 @@ constexpr int kDqk = MISA_MLA_DQK, kDv = MISA_MLA_DV;
 constexpr int kTile = 128;                        // rows of a tile
 constexpr int kHeads = 64;                        // heads of a CTA
 constexpr int kBlocks = kDqk / 64;                // 9
-constexpr int kBlockBytes = 64 * 128;             // 64 rows (heads) x 64 bf16
-constexpr int kKUnits = 3, kKUnitBlocks = 3;      // ring of S operands: one tile
-constexpr int kVUnits = 4, kVUnitRows = 32;       // ring of O operands: one tile
-constexpr int kVAtom = kVUnitRows * 128;          // 32 rows x 64 entries
-constexpr int kVUnitBytes = 4 * kVAtom;           // 32 rows x 256 entries
-constexpr int kOffQ = 0;
-constexpr int kOffK = kOffQ + kBlocks * kBlockBytes;
-constexpr int kOffV = kOffK + kBlocks * kBlockBytes;
-constexpr int kOffP = kOffV + kVUnits * kVUnitBytes;
-constexpr int kOffBar = kOffP + 2 * kBlockBytes;
-constexpr int kNumBars = 2 * kKUnits + 2 * kVUnits + 2 + 2 + 5;
-constexpr int kOffTmem = kOffBar + kNumBars * 8;
-constexpr int kOffAbort = kOffTmem + 8;
-constexpr int kOffRed = (kOffAbort + 8 + 15) / 16 * 16;   // [2][128] floats
+constexpr uint32_t kBlockBytes = 64 * 128;        // 64 rows (heads) x 64 bf16
+constexpr int kKUnits = 5;                        // S operand: four pairs of blocks, then the rotary block
+constexpr int kVUnits = 4;                        // O operand: 32 rows x 256 entries each
+constexpr uint32_t kVAtom = 32 * 128;             // 32 rows x 64 entries
+constexpr uint32_t kVUnitBytes = 4 * kVAtom;
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = kOffQ + kBlocks * kBlockBytes;
+constexpr uint32_t kOffV = kOffK + kBlocks * kBlockBytes;
+constexpr uint32_t kOffP = kOffV + kVUnits * kVUnitBytes;
+constexpr uint32_t kOffBar = kOffP + 2 * kBlockBytes;
+// barriers (of the first CTA where it says so)
+constexpr uint32_t kKFull = kOffBar;              // [5] first CTA: unit brought by both
+constexpr uint32_t kKEmpty = kKFull + 8 * kKUnits;   // [5] multiplied
+constexpr uint32_t kVFull = kKEmpty + 8 * kKUnits;   // [4] first CTA
+constexpr uint32_t kVEmpty = kVFull + 8 * kVUnits;   // [4]
+constexpr uint32_t kLanded = kVEmpty + 8 * kVUnits;  // [9] bf16: TMA done, S units then O units
+constexpr uint32_t kSFull = kLanded + 8 * (kKUnits + kVUnits);   // [2] S complete
+constexpr uint32_t kSEmpty = kSFull + 16;         // [2] first CTA: S read by both
+constexpr uint32_t kPFull = kSEmpty + 16;         // first CTA: P written (and O scaled) by both
+constexpr uint32_t kPvDone = kPFull + 8;          // O += P V complete
+constexpr uint32_t kQFull = kPvDone + 8;          // this CTA's queries landed
+constexpr uint32_t kQReady = kQFull + 8;          // first CTA: both CTAs' queries landed
+constexpr uint32_t kDone = kQReady + 8;           // every MMA retired
+constexpr uint32_t kOffTmem = kDone + 8;
+constexpr uint32_t kOffAbort = kOffTmem + 8;
+constexpr uint32_t kOffRed = (kOffAbort + 8 + 15) / 16 * 16;   // [2][128] floats
 constexpr int kSmemBytes = kOffRed + 2 * 128 * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 constexpr int kMmaWarp = 4, kKWarp0 = 5, kVWarp0 = 9, kThreads = 13 * 32;
-constexpr int kTmemS = 256;                       // O: columns 0..255, S: two places of 64 columns
+constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 64 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
+
+// ---------------------------------------------------------------- shared memory by address
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Arrive on CTA `rank`'s barrier.  The release is the CTA's: what this warp wrote is
+// its own CTA's shared memory, which its own SM's tensor core reads, and
+// fence.proxy.async has ordered that.  (A release of the cluster's scope would wait
+// for the loads under way and for a round trip to L2, about 1000 cycles.)
+__device__ __forceinline__ void arrive_in(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar),
+      "r"(rank)
+      : "memory");
+}
+// Whether the phase of `parity` is over (test: without waiting at all).
+__device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t ld_shared(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Gives up once a wait has taken about two seconds, or another one of the CTA has.
+struct Patience {
+  uint64_t t0;
+  int spins;
+  __device__ __forceinline__ bool more(uint32_t sb, uint32_t* err) {
+    if ((++spins & 31) != 0) return true;
+    if (ld_shared(sb + kOffAbort)) return false;
+    const uint64_t now = globaltimer_ns();
+    if (spins == 32) t0 = now;
+    if (now - t0 <= kWaitLimitNs) return true;
+    record_error(err, MISA_DEVERR_TIMEOUT);
+    st_shared(sb + kOffAbort, 1u);
+    return false;
+  }
+};
+__device__ __forceinline__ bool wait_one(uint32_t sb, uint32_t bar, uint32_t parity, uint32_t* err) {
+  Patience left = {0, 0};
+  while (!try_phase(bar, parity))
+    if (!left.more(sb, err)) return false;
+  return true;
+}
+// A wait of a whole warp: one outcome for all lanes.
+__device__ __forceinline__ bool wait_warp(uint32_t sb, uint32_t bar, uint32_t parity, uint32_t* err) {
+  return __all_sync(0xffffffffu, wait_one(sb, bar, parity, err));
+}
 
 // ---------------------------------------------------------------- the pair
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -75,20 +169,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// Arrive on the first CTA's barrier.  The release is the CTA's: what this warp
-// wrote is its own CTA's shared memory, which its own SM's tensor core reads, and
-// fence.proxy.async has ordered that.  (A release of the cluster's scope would wait
-// for the loads of the next unit and for a round trip to L2, about 1000 cycles.)
-__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-// A wait of a whole warp: one outcome for all lanes.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err, volatile uint32_t* abort) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort));
-}
 __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -97,10 +177,9 @@ __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 // Arrive on this barrier of both CTAs when the MMAs issued so far are done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
@@ -112,6 +191,18 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t lbo) {
   return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const void* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const void* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
   tmem_ld16(taddr, r);
@@ -142,6 +233,7 @@ __device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefe
 struct Work {
   int t;
   int n, tile0, tile1;
+  int seq;
   const uint8_t* base;      // cache of the query's sequence
   const int32_t* idx;       // its listed rows, or NULL: slot s is row s
   int64_t L;
@@ -162,237 +254,197 @@ __device__ __forceinline__ uint2 load_code(const uint8_t* row, int entry) {   //
 
 // Signals a unit: this lane's writes are visible to the tensor core, and the warp
 // arrives once.
-__device__ __forceinline__ void unit_ready(uint64_t* bar) {
+__device__ __forceinline__ void unit_ready(uint32_t full) {
   fence_proxy_async_smem();
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) arrive_leader(bar);
+  if ((threadIdx.x & 31) == 0) arrive_in(full, 0);
 }
 
-// Brings the S operand, 128 threads: thread = (row r0 + 16 i, piece) of each block.
+// Brings quantised rows for S, 128 threads: thread = (rows r0 + 16 i, piece of 8
+// entries) of each block.  An absent row is any row's codes with a scale of zero.
 template <int kFmt>
-__device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid, uint8_t* sK, uint64_t* full,
-                                           uint64_t* empty, uint32_t* err, volatile uint32_t* abort) {
+__device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid, uint32_t sb, uint32_t* err) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7;
-  uint8_t* dst0 = sK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 16 apart: the same swizzle
+  const uint32_t dst0 = sb + kOffK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 16 apart: the same swizzle
   const int own = static_cast<int>(rank) * 64;
+  const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
+  // the rows two tiles ahead into L2: lines of 128 bytes, two threads a row
   auto prefetch = [&](int tile) {
-    // (lines of 128 bytes, two threads a row; one bulk prefetch a row is issued lane
-    // by lane and took a warp 3000 cycles a tile)
     if (tile >= w.tile1) return;
     const int32_t id = row_of(w, tile * kTile + own + (tid >> 1));
     if (id < 0) return;
-    const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow;
+    const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow + (tid & 1) * 128;
 #pragma unroll
     for (int o = 0; o < kRow; o += 256)
-      if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o + (tid & 1) * 128);
+      if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o);
+  };
+  int32_t id[4];
+  const uint8_t* src[4];
+  bool here[4];
+  auto load_ids = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = tile < w.tile1 ? row_of(w, tile * kTile + own + r0 + 16 * i) : -1;
+  };
+  auto point = [&] {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      here[i] = id[i] >= 0;
+      src[i] = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;
+    }
+  };
+  uint2 cur[8];
+  uint32_t scale[4];
+  auto load_pair = [&](int u, uint2* c, uint32_t* s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] = 0u;
+      if (here[i]) s[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i] + kv_code_bytes(kFmt) + 4 * u));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) c[x * 4 + i] = load_code<kFmt>(src[i], u * 128 + x * 64 + piece * 8);
+    }
   };
   prefetch(w.tile0);
   prefetch(w.tile0 + 1);
-  int32_t ids[4];
-  auto load_ids = [&](int tile) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ids[i] = tile < w.tile1 ? row_of(w, tile * kTile + own + r0 + 16 * i) : -1;
-  };
   load_ids(w.tile0);
-
-  if constexpr (kFmt == MISA_KV_BF16) {
-    int pending = -1;   // unit whose copies are under way
-    uint32_t ph = 0;
-    for (int tile = w.tile0; tile < w.tile1; ++tile, ph ^= 1u) {
-      prefetch(tile + 2);
-      const uint8_t* src[4];
+  point();
+  load_pair(0, cur, scale);
+  load_ids(w.tile0 + 1);
+  uint32_t parity = 1;
+  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u) {
+    prefetch(tile + 2);
+    uint4 rope[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) src[i] = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow + piece * 16;
-      for (int g = 0; g < kKUnits; ++g) {
-        if (pending >= 0 && !__all_sync(0xffffffffu, mbar_try_wait(&empty[g], ph ^ 1u))) {
-          cp_async_wait_group<0>();
-          unit_ready(&full[pending]);
-          pending = -1;
-        }
-        if (!wait_warp(&empty[g], ph ^ 1u, err, abort)) { cp_async_wait_group<0>(); return; }
-#pragma unroll
-        for (int bb = 0; bb < kKUnitBlocks; ++bb) {
-          const int b = g * kKUnitBlocks + bb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cp_async_16(dst0 + b * kBlockBytes + i * 2048, src[i] + b * 128, ids[i] >= 0);
-        }
-        cp_async_commit();
-        if (pending >= 0) {
-          cp_async_wait_group<1>();
-          unit_ready(&full[pending]);
-        }
-        pending = g;
-      }
-      load_ids(tile + 1);
+    for (int i = 0; i < 4; ++i) {
+      rope[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (here[i]) rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
     }
-    cp_async_wait_group<0>();
-    if (pending >= 0) unit_ready(&full[pending]);
-  } else {
-    // Absent rows: any row's codes with scales of zero, and no rotary entries.
-    uint2 cur[kKUnitBlocks * 4];    // codes of the unit at hand (the rotary block apart)
-    uint4 rope[4], scales[4];
-    bool absent[4];
-    const uint8_t* src[4];
-    auto point = [&] {
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+      uint2 next[8];
+      uint32_t nscale[4];
+      if (u == 3) point();
+      load_pair((u + 1) & 3, next, nscale);
+      if (!wait_warp(sb, sb + kKEmpty + 8 * u, parity, err)) return;
+      const uint32_t dst = dst0 + u * 2 * kBlockBytes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) src[i] = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow;
-    };
-    auto load_unit = [&](int g, uint2* c) {
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int bb = 0; bb < kKUnitBlocks; ++bb) {
-        const int b = g * kKUnitBlocks + bb;
-        if (b == kBlocks - 1) continue;
+        for (int i = 0; i < 4; ++i)
+          st_shared16(dst + x * kBlockBytes + i * 2048,
+                      kv_decode8<kFmt>(cur[x * 4 + i].x, cur[x * 4 + i].y, kv_scale(__byte_perm(scale[i], 0u, sel + 2 * x))));
+      unit_ready(sb + kKFull + 8 * u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[bb * 4 + i] = load_code<kFmt>(src[i], b * 64 + piece * 8);
-      }
-    };
-    auto load_rest = [&] {
+      for (int j = 0; j < 8; ++j) cur[j] = next[j];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        scales[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_code_bytes(kFmt)));
-        rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
-        absent[i] = ids[i] < 0;
-      }
-    };
-    point();
-    load_unit(0, cur);
-    load_rest();
-    load_ids(w.tile0 + 1);
-    const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
-    uint32_t ph = 0;
-    for (int tile = w.tile0; tile < w.tile1; ++tile, ph ^= 1u) {
-      prefetch(tile + 2);
-#pragma unroll
-      for (int g = 0; g < kKUnits; ++g) {
-        uint2 nxt[kKUnitBlocks * 4];
-        if (g + 1 < kKUnits) {
-          load_unit(g + 1, nxt);
-        } else {
-          point();
-          load_unit(0, nxt);
-        }
-        if (!wait_warp(&empty[g], ph ^ 1u, err, abort)) return;
-        if (g == 0) {   // (here, not where they are loaded: this waits for them)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (absent[i]) scales[i] = rope[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int bb = 0; bb < kKUnitBlocks; ++bb) {
-          const int b = g * kKUnitBlocks + bb;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 y;
-            if (b == kBlocks - 1) {
-              y = rope[i];
-            } else {
-              const uint32_t sw = b < 2 ? scales[i].x : b < 4 ? scales[i].y : b < 6 ? scales[i].z : scales[i].w;
-              const uint2 c = cur[bb * 4 + i];
-              y = kv_decode8<kFmt>(c.x, c.y, kv_scale(__byte_perm(sw, 0u, sel + (b & 1) * 2)));
-            }
-            *reinterpret_cast<uint4*>(dst0 + b * kBlockBytes + i * 2048) = y;
-          }
-        }
-        unit_ready(&full[g]);
-#pragma unroll
-        for (int j = 0; j < kKUnitBlocks * 4; ++j) cur[j] = nxt[j];
-      }
-      load_rest();                // of the rows `src` points at now
-      load_ids(tile + 2);
+      for (int i = 0; i < 4; ++i) scale[i] = nscale[i];
     }
+    load_ids(tile + 2);
+    if (!wait_warp(sb, sb + kKEmpty + 8 * 4, parity, err)) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 2048, rope[i]);
+    unit_ready(sb + kKFull + 8 * 4);
   }
 }
 
-// Brings the O operand, 128 threads: entries [256 rank, 256 rank + 256) of units of 32 rows.
+// Brings quantised rows for O, 128 threads: entries [256 rank, 256 rank + 256) of 32 rows a unit.
 template <int kFmt>
-__device__ __forceinline__ void bring_values(const Work& w, uint32_t rank, int tid, uint8_t* sV, uint64_t* full,
-                                             uint64_t* empty, uint32_t* err, volatile uint32_t* abort) {
+__device__ __forceinline__ void bring_values(const Work& w, uint32_t rank, int tid, uint32_t sb, uint32_t* err) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7;
-  uint8_t* dst0 = sV + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
-  int32_t ids[2];
-  auto load_ids = [&](int tile, int g) {
+  const uint32_t dst0 = sb + kOffV + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+  const uint32_t sel = 0x4440u | (piece >> 2);
+  int32_t id[2];
+  auto load_ids = [&](int unit) {   // unit: counted over the tiles
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      ids[i] = tile < w.tile1 ? row_of(w, tile * kTile + g * kVUnitRows + r0 + 16 * i) : -1;
+    for (int i = 0; i < 2; ++i) id[i] = unit < w.tile1 * kVUnits ? row_of(w, unit * 32 + r0 + 16 * i) : -1;
   };
-  load_ids(w.tile0, 0);
-
-  if constexpr (kFmt == MISA_KV_BF16) {
-    int pending = -1;
-    uint32_t ph = 0;
-    for (int tile = w.tile0; tile < w.tile1; ++tile, ph ^= 1u) {
-      for (int g = 0; g < kVUnits; ++g) {
-        if (pending >= 0 && !__all_sync(0xffffffffu, mbar_try_wait(&empty[g], ph ^ 1u))) {
-          cp_async_wait_group<0>();
-          unit_ready(&full[pending]);
-          pending = -1;
-        }
-        if (!wait_warp(&empty[g], ph ^ 1u, err, abort)) { cp_async_wait_group<0>(); return; }
+  uint2 cur[8], scale[2];
+  auto load_unit = [&](uint2* c, uint2* s) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* src = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow + rank * 512 + piece * 16;
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t* src = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;
+      s[i] = make_uint2(0u, 0u);
+      if (id[i] >= 0) s[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
 #pragma unroll
-          for (int a = 0; a < 4; ++a) cp_async_16(dst0 + g * kVUnitBytes + a * kVAtom + i * 2048, src + a * 128, ids[i] >= 0);
-        }
-        cp_async_commit();
-        if (pending >= 0) {
-          cp_async_wait_group<1>();
-          unit_ready(&full[pending]);
-        }
-        pending = g;
-        if (g + 1 < kVUnits) load_ids(tile, g + 1);
-        else load_ids(tile + 1, 0);
-      }
+      for (int a = 0; a < 4; ++a) c[i * 4 + a] = load_code<kFmt>(src, static_cast<int>(rank) * 256 + a * 64 + piece * 8);
     }
-    cp_async_wait_group<0>();
-    if (pending >= 0) unit_ready(&full[pending]);
-  } else {
-    uint2 cur[8], scales[2];
-    const uint8_t* src[2];
-    bool absent[2];
-    auto load_unit = [&](uint2* c, uint2* s) {   // of the rows `ids`
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        src[i] = w.base + static_cast<int64_t>(max(ids[i], 0)) * kRow;
-        s[i] = __ldg(reinterpret_cast<const uint2*>(src[i] + kv_code_bytes(kFmt) + rank * 8));
-        absent[i] = ids[i] < 0;
-#pragma unroll
-        for (int a = 0; a < 4; ++a) c[i * 4 + a] = load_code<kFmt>(src[i], static_cast<int>(rank) * 256 + a * 64 + piece * 8);
-      }
-    };
-    load_unit(cur, scales);
+  };
+  int unit = w.tile0 * kVUnits;
+  load_ids(unit);
+  load_unit(cur, scale);
+  load_ids(unit + 1);
+  const int first = unit;
+#pragma unroll 1
+  for (; unit < w.tile1 * kVUnits; ++unit) {
+    const int g = unit & (kVUnits - 1);
+    uint2 next[8], nscale[2];
+    load_unit(next, nscale);
+    load_ids(unit + 2);
+    if (!wait_warp(sb, sb + kVEmpty + 8 * g, (((unit - first) >> 2) & 1) ^ 1u, err)) return;
+    const uint32_t dst = dst0 + g * kVUnitBytes;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (absent[i]) scales[i] = make_uint2(0u, 0u);
-    load_ids(w.tile0, 1);
-    const uint32_t sel = 0x4440u | (piece >> 2);
-    uint32_t ph = 0;
-    for (int tile = w.tile0; tile < w.tile1; ++tile, ph ^= 1u) {
 #pragma unroll
-      for (int g = 0; g < kVUnits; ++g) {
-        uint2 nxt[8], nscales[2];
-        load_unit(nxt, nscales);
-        if (g + 2 < kVUnits) load_ids(tile, g + 2);
-        else load_ids(tile + 1, g + 2 - kVUnits);
-        if (!wait_warp(&empty[g], ph ^ 1u, err, abort)) return;
+      for (int a = 0; a < 4; ++a)
+        st_shared16(dst + a * kVAtom + i * 2048,
+                    kv_decode8<kFmt>(cur[i * 4 + a].x, cur[i * 4 + a].y,
+                                     kv_scale(__byte_perm(a < 2 ? scale[i].x : scale[i].y, 0u, sel + 2 * (a & 1)))));
+    unit_ready(sb + kVFull + 8 * g);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            const uint2 c = cur[i * 4 + a];
-            *reinterpret_cast<uint4*>(dst0 + g * kVUnitBytes + a * kVAtom + i * 2048) =
-                kv_decode8<kFmt>(c.x, c.y, kv_scale(__byte_perm(a < 2 ? scales[i].x : scales[i].y, 0u, sel + (a & 1) * 2)));
-          }
-        unit_ready(&full[g]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) scales[i] = absent[i] ? make_uint2(0u, 0u) : nscales[i];
-      }
-    }
+    for (int j = 0; j < 8; ++j) cur[j] = next[j];
+    scale[0] = nscale[0];
+    scale[1] = nscale[1];
   }
+}
+
+// Brings bf16 rows by TMA: one thread asks for those of S and one for those of O,
+// and a warp each passes on what has landed.  Rows behind the prefix are cleared in
+// O's operand: P is 0 there, but 0 times a stale NaN is not.
+__device__ __forceinline__ void ask_keys(const Work& w, uint32_t rank, const CUtensorMap* map, uint32_t sb, uint32_t* err) {
+  uint32_t parity = 1;
+  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
+    for (int u = 0; u < kKUnits; ++u) {
+      if (!wait_one(sb, sb + kKEmpty + 8 * u, parity, err)) return;
+      const uint32_t bar = sb + kLanded + 8 * u;
+      const int nb = u < 4 ? 2 : 1;
+      bar_expect(bar, nb * kBlockBytes);
+      for (int x = 0; x < nb; ++x)
+        for (int h = 0; h < 2; ++h)   // 32 rows
+          tma_3d(sb + kOffK + (2 * u + x) * kBlockBytes + h * kVAtom, map, bar, (2 * u + x) * 64,
+                 tile * kTile + static_cast<int>(rank) * 64 + h * 32, w.seq);
+    }
+}
+__device__ __forceinline__ void ask_values(const Work& w, uint32_t rank, const CUtensorMap* map, uint32_t sb, uint32_t* err) {
+  uint32_t parity = 1;
+  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
+    for (int g = 0; g < kVUnits; ++g) {
+      if (!wait_one(sb, sb + kVEmpty + 8 * g, parity, err)) return;
+      const uint32_t bar = sb + kLanded + 8 * (kKUnits + g);
+      bar_expect(bar, kVUnitBytes);
+      for (int a = 0; a < 4; ++a)
+        tma_3d(sb + kOffV + g * kVUnitBytes + a * kVAtom, map, bar, static_cast<int>(rank) * 256 + a * 64, tile * kTile + g * 32, w.seq);
+    }
+}
+__device__ __forceinline__ void pass_keys(const Work& w, uint32_t sb, uint32_t* err) {
+  uint32_t parity = 0;
+  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
+    for (int u = 0; u < kKUnits; ++u) {
+      if (!wait_one(sb, sb + kLanded + 8 * u, parity, err)) return;
+      arrive_in(sb + kKFull + 8 * u, 0);
+    }
+}
+__device__ __forceinline__ void pass_values(const Work& w, int lane, uint32_t sb, uint32_t* err) {
+  uint32_t parity = 0;
+  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
+    for (int g = 0; g < kVUnits; ++g) {
+      if (!wait_warp(sb, sb + kLanded + 8 * (kKUnits + g), parity, err)) return;
+      const int live = min(max(w.n - tile * kTile - g * 32, 0), 32);   // rows of this unit that exist
+      for (int a = 0; a < 4; ++a)
+        for (int c = live * 8 + lane; c < 32 * 8; c += 32)   // whole rows: the swizzle does not matter
+          st_shared16(sb + kOffV + g * kVUnitBytes + a * kVAtom + c * 16, make_uint4(0u, 0u, 0u, 0u));
+      unit_ready(sb + kVFull + 8 * g);
+    }
 }
 
 struct MlaParams {
@@ -404,50 +456,39 @@ struct MlaParams {
 
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) {
+latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap row_map, const MlaParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *sQ = smem + kOffQ, *sK = smem + kOffK, *sV = smem + kOffV, *sP = smem + kOffP;
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + kOffBar);   // first CTA: unit brought by both
-  uint64_t* kempty = kfull + kKUnits;    // unit multiplied
-  uint64_t* vfull = kempty + kKUnits;    // first CTA
-  uint64_t* vempty = vfull + kVUnits;
-  uint64_t* sfull = vempty + kVUnits;    // [2] S complete
-  uint64_t* sempty = sfull + 2;          // [2] first CTA: S read by both
-  uint64_t* pfull = sempty + 2;          // first CTA: P written (and O scaled) by both
-  uint64_t* pvdone = pfull + 1;          // O += P V complete
-  uint64_t* qfull = pfull + 2;           // this CTA's queries landed
-  uint64_t* qready = pfull + 3;          // first CTA: both CTAs' queries landed
-  uint64_t* done = pfull + 4;            // every MMA retired
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffTmem);
-  volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + kOffAbort);
-  float* sRed = reinterpret_cast<float*>(smem + kOffRed);
-
+  const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int item = static_cast<int>(blockIdx.x >> 1);
   if (tid == 0) {
-    for (int i = 0; i < kKUnits; ++i) { mbar_init(&kfull[i], 8); mbar_init(&kempty[i], 1); }
-    for (int i = 0; i < kVUnits; ++i) { mbar_init(&vfull[i], 8); mbar_init(&vempty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&sfull[i], 1); mbar_init(&sempty[i], 8); }
-    mbar_init(pfull, 8);
-    mbar_init(pvdone, 1);
-    mbar_init(qfull, 1);
-    mbar_init(qready, 2);
-    mbar_init(done, 1);
-    *abort = 0u;
+    constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 2 : 8;   // arriving warps of both CTAs
+    for (int i = 0; i < kKUnits; ++i) { bar_init(sb + kKFull + 8 * i, kWriters); bar_init(sb + kKEmpty + 8 * i, 1); }
+    for (int i = 0; i < kVUnits; ++i) { bar_init(sb + kVFull + 8 * i, kWriters); bar_init(sb + kVEmpty + 8 * i, 1); }
+    for (int i = 0; i < kKUnits + kVUnits; ++i) bar_init(sb + kLanded + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) { bar_init(sb + kSFull + 8 * i, 1); bar_init(sb + kSEmpty + 8 * i, 8); }
+    bar_init(sb + kPFull, 8);
+    bar_init(sb + kPvDone, 1);
+    bar_init(sb + kQFull, 1);
+    bar_init(sb + kQReady, 2);
+    bar_init(sb + kDone, 1);
+    st_shared(sb + kOffAbort, 0u);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sb + kOffTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    if (lane == 0) tma_prefetch_desc(&q_map);
+    if (lane == 0) {
+      tma_prefetch_desc(&q_map);
+      if (kFmt == MISA_KV_BF16) tma_prefetch_desc(&row_map);
+    }
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // the other CTA's barriers are ready for arrivals
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = ld_shared(sb + kOffTmem);
   pdl_wait_inputs();
   pdl_allow_next();
 
@@ -466,6 +507,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
     n = 0;
   }
   w.n = static_cast<int>(max(n, static_cast<int64_t>(0)));
+  w.seq = static_cast<int>(seq);
   w.base = static_cast<const uint8_t*>(a.cache) + seq * a.seq_stride;
   const int tiles = (w.n + kTile - 1) / kTile;
   const int share = (tiles + p.nsplit - 1) / p.nsplit;
@@ -474,70 +516,89 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
   const int ntiles = w.tile1 - w.tile0;
 
   if (warp >= kVWarp0) {
-    if (ntiles > 0) bring_values<kFmt>(w, rank, tid - kVWarp0 * 32, sV, vfull, vempty, err, abort);
+    if (ntiles > 0) {
+      if constexpr (kFmt == MISA_KV_BF16) {
+        if (warp == kVWarp0 && elect_one()) ask_values(w, rank, &row_map, sb, err);
+        if (warp == kVWarp0 + 1) pass_values(w, lane, sb, err);
+      } else {
+        bring_values<kFmt>(w, rank, tid - kVWarp0 * 32, sb, err);
+      }
+    }
   } else if (warp >= kKWarp0) {
     if (ntiles > 0) {
-      // ids that name no row: each slot is looked at by one thread of its CTA
-      if (w.idx) {
-        for (int s = w.tile0 * kTile + tid - kKWarp0 * 32; s < min(w.n, w.tile1 * kTile); s += 128)
-          if (rank == 0 && (w.idx[s] < -1 || w.idx[s] >= w.L)) record_error(err, MISA_DEVERR_BAD_INDEX);
+      if constexpr (kFmt == MISA_KV_BF16) {
+        if (warp == kKWarp0 && elect_one()) ask_keys(w, rank, &row_map, sb, err);
+        if (warp == kKWarp0 + 1 && elect_one()) pass_keys(w, sb, err);
+      } else {
+        // ids that name no row: each slot is looked at by one thread of the first CTA
+        if (w.idx && rank == 0) {
+          for (int s = w.tile0 * kTile + tid - kKWarp0 * 32; s < min(w.n, w.tile1 * kTile); s += 128)
+            if (w.idx[s] < -1 || w.idx[s] >= w.L) record_error(err, MISA_DEVERR_BAD_INDEX);
+        }
+        bring_keys<kFmt>(w, rank, tid - kKWarp0 * 32, sb, err);
       }
-      bring_keys<kFmt>(w, rank, tid - kKWarp0 * 32, sK, kfull, kempty, err, abort);
     }
   } else if (warp == kMmaWarp) {
     if (ntiles > 0 && elect_one()) {
-      mbar_arrive_expect_tx(qfull, kBlocks * kBlockBytes);
+      bar_expect(sb + kQFull, kBlocks * kBlockBytes);
       for (int b = 0; b < kBlocks; ++b)
-        tma_load_2d(sQ + b * kBlockBytes, &q_map, qfull, b * 64, w.t * a.Hq + static_cast<int>(rank) * kHeads);
-      const bool landed = mbar_wait(qfull, 0, err, abort);
-      if (landed) arrive_leader(qready);
+        tma_2d(sb + kOffQ + b * kBlockBytes, &q_map, sb + kQFull, b * 64, w.t * a.Hq + static_cast<int>(rank) * kHeads);
+      bool ok = wait_one(sb, sb + kQFull, 0, err);
+      if (ok) arrive_in(sb + kQReady, 0);
       if (rank == 0) {
-        const uint32_t qa = smem_u32(sQ), ka = smem_u32(sK), va = smem_u32(sV), pa = smem_u32(sP);
-        auto scores = [&](int i) {   // S of tile i (counted from the cluster's first)
-          if (!mbar_wait(&sempty[i & 1], ((i >> 1) & 1) ^ 1u, err, abort)) return false;
-          const uint32_t d = tmem + kTmemS + (i & 1) * 64;
-          for (int g = 0; g < kKUnits; ++g) {
-            if (!mbar_wait(&kfull[g], i & 1, err, abort)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int bb = 0; bb < kKUnitBlocks; ++bb)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint32_t at = (g * kKUnitBlocks + bb) * kBlockBytes + kk * 32;
-                umma_pair(d, sw128_kmajor_desc(qa + at), sw128_kmajor_desc(ka + at), kIdescS, (g | bb | kk) ? 1u : 0u);
-              }
-            commit_pair(&kempty[g]);
-          }
-          commit_pair(&sfull[i & 1]);
-          return true;
-        };
-        auto values = [&](int i) {
-          if (!mbar_wait(pfull, i & 1, err, abort)) return false;
-          for (int g = 0; g < kVUnits; ++g) {
-            if (!mbar_wait(&vfull[g], i & 1, err, abort)) return false;
+        // Two rows of work, S of tile s unit by unit and O += P V of tile o unit by
+        // unit; whatever has its operands next is issued, O first.
+        ok = ok && wait_one(sb, sb + kQReady, 0, err);
+        int s_tile = 0, s_unit = 0, o_tile = 0, o_unit = 0;
+        Patience left = {0, 0};
+        while (ok && o_tile < ntiles) {
+          if (o_tile < s_tile && (o_unit || test_phase(sb + kPFull, o_tile & 1)) &&
+              test_phase(sb + kVFull + 8 * o_unit, o_tile & 1)) {
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-              const int step = g * 2 + kk;   // 16 rows
-              const uint64_t ad = sw128_kmajor_desc(pa + (step >> 2) * kBlockBytes + (step & 3) * 32);
+              const int step = o_unit * 2 + kk;   // 16 rows
+              const uint64_t ad = sw128_kmajor_desc(sb + kOffP + (step >> 2) * kBlockBytes + (step & 3) * 32);
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                umma_pair(tmem + j * 128, ad, sw128_mnmajor_desc(va + g * kVUnitBytes + j * 2 * kVAtom + kk * 2048, kVAtom),
-                          kIdescO, (i | step) ? 1u : 0u);
+                umma_pair(tmem + j * 128, ad,
+                          sw128_mnmajor_desc(sb + kOffV + o_unit * kVUnitBytes + j * 2 * kVAtom + kk * 2048, kVAtom), kIdescO,
+                          (o_tile | step) ? 1u : 0u);
             }
-            commit_pair(&vempty[g]);
+            commit_pair(sb + kVEmpty + 8 * o_unit);
+            if (++o_unit == kVUnits) {
+              commit_pair(sb + kPvDone);
+              o_unit = 0;
+              ++o_tile;
+            }
+            left.spins = 0;
+          } else if (s_tile < ntiles && (s_unit || test_phase(sb + kSEmpty + 8 * (s_tile & 1), ((s_tile >> 1) & 1) ^ 1u)) &&
+                     test_phase(sb + kKFull + 8 * s_unit, s_tile & 1)) {
+            tc_fence_after();
+            const uint32_t d = tmem + kTmemS + (s_tile & 1) * 64;
+#pragma unroll 1
+            for (int x = 0; x < (s_unit < 4 ? 2 : 1); ++x) {
+              const uint32_t at = (2 * s_unit + x) * kBlockBytes;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_pair(d, sw128_kmajor_desc(sb + kOffQ + at + kk * 32), sw128_kmajor_desc(sb + kOffK + at + kk * 32),
+                          kIdescS, (s_unit | x | kk) ? 1u : 0u);
+            }
+            commit_pair(sb + kKEmpty + 8 * s_unit);
+            if (++s_unit == kKUnits) {
+              commit_pair(sb + kSFull + 8 * (s_tile & 1));
+              s_unit = 0;
+              ++s_tile;
+            }
+            left.spins = 0;
+          } else {
+            ok = left.more(sb, err);
           }
-          commit_pair(pvdone);
-          return true;
-        };
-        bool ok = landed && mbar_wait(qready, 0, err, abort) && scores(0);
-        for (int i = 0; i < ntiles && ok; ++i) {
-          if (i + 1 < ntiles) ok = scores(i + 1);
-          ok = ok && values(i);
         }
-        commit_pair(done);
+        commit_pair(sb + kDone);
       }
-      mbar_wait(done, 0, err, nullptr);   // both: nothing reads this CTA's memory any more
+      // both: nothing reads this CTA's memory any more
+      if (!wait_one(sb, sb + kDone, 0, err)) ok = false;
     }
     __syncwarp();
   } else {
@@ -547,7 +608,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
     const int h = static_cast<int>(rank) * kHeads + hl;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float kNegInf = -__int_as_float(0x7f800000);
-    const float c = a.scale_log2;
+    const float c = fmaxf(a.scale_log2, 1.2e-38f);   // a scale of 0 weighs all rows alike; -inf stays -inf
     float m = kNegInf, l = 0.f;
     bool ok = true;
     for (int i = 0; i < ntiles; ++i) {
@@ -557,7 +618,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
       for (int j = 0; j < 2; ++j)
         live[j] = __ballot_sync(0xffffffffu, row_of(w, (w.tile0 + i) * kTile + half * 64 + j * 32 + lane) >= 0);
       // a wait that gave up ends the work, not the loop: the warps' barriers stay paired
-      ok = ok && wait_warp(&sfull[i & 1], (i >> 1) & 1, err, abort);
+      ok = ok && wait_warp(sb, sb + kSFull + 8 * (i & 1), (i >> 1) & 1, err);
       uint32_t s[64];
       if (ok) {
         tc_fence_after();
@@ -566,25 +627,21 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(&sempty[i & 1]);
+        if (lane == 0) arrive_in(sb + kSEmpty + 8 * (i & 1), 0);
       }
-      float mx = kNegInf;
-      if ((live[0] & live[1]) == 0xffffffffu) {
+      if ((live[0] & live[1]) != 0xffffffffu) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) {
+        for (int j = 0; j < 64; ++j)
           if (!((live[j >> 5] >> (j & 31)) & 1u)) s[j] = 0xff800000u;
-          mx = fmaxf(mx, __uint_as_float(s[j]));
-        }
       }
+      float mx = __uint_as_float(s[0]);
+#pragma unroll
+      for (int j = 1; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
       // the other half of the tile's rows for the same head
-      float* red = sRed + (i & 1) * 128;
-      red[warp * 32 + lane] = mx;
+      const uint32_t red = sb + kOffRed + (i & 1) * 512;
+      st_shared(red + tid * 4, __float_as_uint(mx));
       named_bar_sync(1, 128);
-      mx = fmaxf(mx, red[((warp ^ 2) * 32) + lane]) * c;
-      if (mx != mx) mx = kNegInf;    // scale 0 and nothing live: 0 * -inf
+      mx = fmaxf(mx, __uint_as_float(ld_shared(red + (tid ^ 64) * 4))) * c;
       float f = 1.f;
       if (mx > m + 8.f || (m == kNegInf && mx > kNegInf)) {
         f = m == kNegInf ? 0.f : ex2(m - mx);
@@ -592,22 +649,16 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
         l *= f;
       }
       const float mr = m == kNegInf ? 0.f : m;
-      uint32_t pk[32];
       float l0 = 0.f, l1 = 0.f;
-      const bool masked = (live[0] & live[1]) != 0xffffffffu;
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {
-        float x = ex2(fmaf(__uint_as_float(s[j]), c, -mr)), y = ex2(fmaf(__uint_as_float(s[j + 1]), c, -mr));
-        if (masked) {
-          if (!((live[j >> 5] >> (j & 31)) & 1u)) x = 0.f;
-          if (!((live[j >> 5] >> ((j & 31) + 1)) & 1u)) y = 0.f;
-        }
+      for (int j = 0; j < 64; j += 2) {   // (the packed pairs take the place of the scores)
+        const float x = ex2(fmaf(__uint_as_float(s[j]), c, -mr)), y = ex2(fmaf(__uint_as_float(s[j + 1]), c, -mr));
         l0 += x;
         l1 += y;
-        pk[j >> 1] = pack_bf16(x, y);
+        s[j >> 1] = pack_bf16(x, y);
       }
       l += l0 + l1;
-      if (i > 0) ok = ok && wait_warp(pvdone, (i - 1) & 1, err, abort);
+      if (i > 0) ok = ok && wait_warp(sb, sb + kPvDone, (i - 1) & 1, err);
       if (!ok) continue;
       if (i > 0) {
         tc_fence_after();
@@ -625,21 +676,22 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const MlaParams p) 
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         }
       }
-      uint8_t* prow = sP + half * kBlockBytes + hl * 128;
+      const uint32_t prow = sb + kOffP + half * kBlockBytes + hl * 128;
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        *reinterpret_cast<uint4*>(prow + ((u ^ (hl & 7)) << 4)) =
-            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        st_shared16(prow + ((u ^ (hl & 7)) << 4), make_uint4(s[4 * u], s[4 * u + 1], s[4 * u + 2], s[4 * u + 3]));
       tc_fence_before();
-      unit_ready(pfull);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_in(sb + kPFull, 0);
     }
     // both halves' sums; a barrier apart from the last tile's exchange
     named_bar_sync(1, 128);
-    sRed[warp * 32 + lane] = l;
+    st_shared(sb + kOffRed + tid * 4, __float_as_uint(l));
     named_bar_sync(1, 128);
-    l += sRed[((warp ^ 2) * 32) + lane];
+    l += __uint_as_float(ld_shared(sb + kOffRed + (tid ^ 64) * 4));
     if (ntiles > 0) {
-      ok = ok && wait_warp(pvdone, (ntiles - 1) & 1, err, abort);
+      ok = ok && wait_warp(sb, sb + kPvDone, (ntiles - 1) & 1, err);
       tc_fence_after();
     }
     const int64_t row = p.nsplit > 1 ? (static_cast<int64_t>(w.t) * p.nsplit + split) * a.Hq + h
@@ -776,12 +828,17 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   CUtensorMap qmap;
   if (!encode_2d_map(&qmap, true, a.q, kDqk, static_cast<uint64_t>(a.T) * a.Hq, kDqk * 2, 64, kHeads, true))
     return cudaErrorInvalidValue;
+  CUtensorMap rmap = qmap;   // (quantised rows go by plain loads)
+  if (a.fmt == MISA_KV_BF16 &&
+      !encode_3d_map(&rmap, a.cache, kDqk, static_cast<uint64_t>(a.L), static_cast<uint64_t>(a.nseq), kDqk * 2,
+                     a.nseq > 1 ? static_cast<uint64_t>(a.seq_stride) : static_cast<uint64_t>(a.L) * kDqk * 2, 64, 32))
+    return cudaErrorInvalidValue;
   auto kern = a.fmt == MISA_KV_BF16  ? latent_mla_kernel<MISA_KV_BF16>
               : a.fmt == MISA_KV_MX8 ? latent_mla_kernel<MISA_KV_MX8>
                                      : latent_mla_kernel<MISA_KV_MX4>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(a.T) * p.nsplit * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, p);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(a.T) * p.nsplit * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * a.Hq), dim3(128), 0, stream, 0,
                     static_cast<const float*>(p.part_o), static_cast<const float*>(p.part_ml), a.Hq, p.nsplit, a.out, a.lse);

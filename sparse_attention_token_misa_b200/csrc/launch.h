@@ -20,6 +20,10 @@ cudaError_t ensure_dynamic_smem(const void* func, int bytes);
 // `row_bytes` apart; box = box_inner x box_rows; optional 128-byte swizzle.
 bool encode_2d_map(CUtensorMap* map, bool bf16, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
                    uint32_t box_inner, uint32_t box_rows, bool swizzle128);
+// 3-D TMA map over `seqs` sequences of `rows` rows of `inner` bf16, 128-byte swizzle;
+// box = box_inner x box_rows x 1.
+bool encode_3d_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t seqs, uint64_t row_bytes,
+                   uint64_t seq_bytes, uint32_t box_inner, uint32_t box_rows);
 // Resident CTAs per SM of `func` at this block size and dynamic shared memory
 // (cached; 1 if the query fails).
 int occupancy_blocks(const void* func, int threads, size_t smem);
