@@ -33,12 +33,17 @@
 // already; copying them there, shared memory to shared memory, instead of bringing
 // them twice was slower (3800 cycles a tile for the copies alone).
 //
-// Few queries: the rows of each are split over several clusters, whose partial
-// sums a second kernel joins in a fixed order.
+// A cluster stays on its SMs and takes every 74th item (a query, or a part of its
+// rows), each role on its own: the rows of the next item come while the output of
+// this one leaves.  (A cluster an item spent 9 us on starting, queries and output
+// around 3 us a tile.)  Few queries: the rows of each are split over several
+// items, whose partial sums a second kernel joins in a fixed order.
 //
-// Roles (416 threads a CTA): warps 0-3 softmax and output (a lane of TMEM each),
-// warp 4 TMEM and, in the first CTA, the MMAs, warps 5-8 bring the rows of S,
-// warps 9-12 those of O.  Shared memory is addressed from one 32-bit base: with a
+// Roles (512 threads a CTA, by warpgroups): warps 0-3 softmax and output (a lane of
+// TMEM each), warps 4-7 bring the rows of S, warps 8-11 those of O, warp 12 has TMEM
+// and, in the first CTA, issues the MMAs, warp 13 brings the queries.  The softmax
+// holds a tile's 64 scores a lane and more, so the last warpgroup gives it 48 of its
+// registers a thread.  Shared memory is addressed from one 32-bit base: with a
 // pointer a barrier the kernel spilled, and what shared memory leaves of L1 does
 // not hold the stack.  Waits are bounded.
 #include "kv_format.cuh"
@@ -73,15 +78,16 @@ constexpr uint32_t kSFull = kLanded + 8 * (kKUnits + kVUnits);   // [2] S comple
 constexpr uint32_t kSEmpty = kSFull + 16;         // [2] first CTA: S read by both
 constexpr uint32_t kPFull = kSEmpty + 16;         // first CTA: P written (and O scaled) by both
 constexpr uint32_t kPvDone = kPFull + 8;          // O += P V complete
-constexpr uint32_t kQFull = kPvDone + 8;          // this CTA's queries landed
+constexpr uint32_t kOEmpty = kPvDone + 8;         // first CTA: O of the item before read by both
+constexpr uint32_t kQFull = kOEmpty + 8;          // this CTA's queries landed
 constexpr uint32_t kQReady = kQFull + 8;          // first CTA: both CTAs' queries landed
-constexpr uint32_t kDone = kQReady + 8;           // every MMA retired
+constexpr uint32_t kQEmpty = kQReady + 8;         // the item's last S complete
+constexpr uint32_t kDone = kQEmpty + 8;           // every MMA retired
 constexpr uint32_t kOffTmem = kDone + 8;
-constexpr uint32_t kOffAbort = kOffTmem + 8;
-constexpr uint32_t kOffRed = (kOffAbort + 8 + 15) / 16 * 16;   // [2][128] floats
-constexpr int kSmemBytes = kOffRed + 2 * 128 * 4 + 1024;
+constexpr uint32_t kOffRed = (kOffTmem + 8 + 15) / 16 * 16;   // [3][128] floats
+constexpr int kSmemBytes = kOffRed + 3 * 128 * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-constexpr int kMmaWarp = 4, kKWarp0 = 5, kVWarp0 = 9, kThreads = 13 * 32;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kQWarp = 13, kThreads = 16 * 32;
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 64 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -104,16 +110,7 @@ __device__ __forceinline__ void arrive_in(uint32_t bar, uint32_t rank) {
       "r"(rank)
       : "memory");
 }
-// Whether the phase of `parity` is over (test: without waiting at all).
-__device__ __forceinline__ bool test_phase(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+// Whether the phase of `parity` is over.
 __device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -134,30 +131,43 @@ __device__ __forceinline__ void st_shared(uint32_t a, uint32_t v) {
 __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// Gives up once a wait has taken about two seconds, or another one of the CTA has.
-struct Patience {
-  uint64_t t0;
-  int spins;
-  __device__ __forceinline__ bool more(uint32_t sb, uint32_t* err) {
-    if ((++spins & 31) != 0) return true;
-    if (ld_shared(sb + kOffAbort)) return false;
-    const uint64_t now = globaltimer_ns();
-    if (spins == 32) t0 = now;
-    if (now - t0 <= kWaitLimitNs) return true;
-    record_error(err, MISA_DEVERR_TIMEOUT);
-    st_shared(sb + kOffAbort, 1u);
-    return false;
-  }
-};
-__device__ __forceinline__ bool wait_one(uint32_t sb, uint32_t bar, uint32_t parity, uint32_t* err) {
-  Patience left = {0, 0};
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// Waits until the phase of `parity` is over; gives up after about two seconds
+// (counted in cycles: the nanosecond timer is read through the pipe that the
+// softmax's exponentials need).
+constexpr uint32_t kWaitCycles = 3900000000u;
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint32_t* err) {
+  if (try_phase(bar, parity)) return true;
+  const uint32_t t0 = clock();
   while (!try_phase(bar, parity))
-    if (!left.more(sb, err)) return false;
+    if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) {
+      record_error(err, MISA_DEVERR_TIMEOUT);
+      return false;
+    }
   return true;
 }
+// The wait at the end of a cluster's work, which may take as long as all of it: its
+// limit counts from the last time that O went on.
+__device__ __forceinline__ void wait_all(uint32_t sb, uint32_t* err) {
+  uint32_t t0 = clock();
+  bool seen = try_phase(sb + kPvDone, 0);
+  while (!try_phase(sb + kDone, 0)) {
+    const bool now = try_phase(sb + kPvDone, 0);
+    if (now != seen) t0 = clock();
+    seen = now;
+    if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) {
+      record_error(err, MISA_DEVERR_TIMEOUT);
+      return;
+    }
+  }
+}
 // A wait of a whole warp: one outcome for all lanes.
-__device__ __forceinline__ bool wait_warp(uint32_t sb, uint32_t bar, uint32_t parity, uint32_t* err) {
-  return __all_sync(0xffffffffu, wait_one(sb, bar, parity, err));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t* err) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, err));
 }
 
 // ---------------------------------------------------------------- the pair
@@ -169,11 +179,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
+// One product with operands kA and kB bytes behind those of the descriptors (added
+// here: worked out ahead of the loop, the descriptors of a tile fill the registers).
+template <uint32_t kA, uint32_t kB>
 __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "add.s64 x, %1, %5;\n\tadd.s64 y, %2, %6;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "n"(kA >> 4), "n"(kB >> 4)
       : "memory");
 }
 // Arrive on this barrier of both CTAs when the MMAs issued so far are done.
@@ -218,7 +232,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));   // (in order: it keeps the registers down)
   return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -226,17 +240,82 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+__device__ __forceinline__ void tma_l2_3d(const void* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 __device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// ---------------------------------------------------------------- rows
-// The work of a cluster: query t, tiles [tile0, tile1) of its n row slots.
+// ---------------------------------------------------------------- items
+struct MlaParams {
+  LatentArgs a;
+  int nsplit, items; // items: T * nsplit
+  uint32_t by_nsplit;   // ceil(2^32 / nsplit) (nsplit > 1)
+  float* part_o;     // [T][nsplit][Hq][512] (nsplit > 1)
+  float* part_ml;    // [T][nsplit][Hq][2]: m (log2 units), l
+};
+// An item: tiles [tile0, tile1) of the n row slots of query t.
 struct Work {
-  int t;
+  int t, split;
   int n, tile0, tile1;
   int seq;
   const uint8_t* base;      // cache of the query's sequence
   const int32_t* idx;       // its listed rows, or NULL: slot s is row s
-  int64_t L;
+  int L;
+};
+// n / nsplit, exact for n * nsplit < 2^32.
+__device__ __forceinline__ int over_splits(const MlaParams& p, int n) {
+  return p.nsplit == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), p.by_nsplit));
+}
+// What global memory says of an item; read early, looked at when the item starts.
+struct Peek {
+  int t, seq, len;
+};
+__device__ __forceinline__ Peek peek(const MlaParams& p, int item) {
+  Peek k = {0, 0, 0};
+  if (item < p.items) {
+    k.t = over_splits(p, item);
+    k.seq = __ldg(p.a.seq_of + k.t);
+    k.len = p.a.idx ? p.a.k : __ldg(p.a.prefix_len + k.t);
+  }
+  return k;
+}
+__device__ __forceinline__ Work work_of(const MlaParams& p, int item, Peek k) {
+  Work w;
+  w.t = k.t;
+  w.split = item - k.t * p.nsplit;
+  w.L = static_cast<int>(p.a.L);
+  w.idx = p.a.idx ? p.a.idx + static_cast<int64_t>(w.t) * p.a.idx_stride : nullptr;
+  w.n = p.a.idx ? k.len : max(min(k.len, w.L), 0);
+  w.seq = k.seq;
+  if (k.seq < 0 || k.seq >= p.a.nseq) w.seq = w.n = 0;
+  w.base = static_cast<const uint8_t*>(p.a.cache) + static_cast<int64_t>(w.seq) * p.a.seq_stride;
+  const int tiles = (w.n + kTile - 1) / kTile;
+  const int share = over_splits(p, tiles + p.nsplit - 1);
+  w.tile0 = min(w.split * share, tiles);
+  w.tile1 = min(w.tile0 + share, tiles);
+  return w;
+}
+// The items of a cluster that have rows, one after the other.
+struct Items {
+  int item, step;
+  Peek ahead;
+  Work w;
+  __device__ __forceinline__ explicit Items(const MlaParams& p) {
+    step = static_cast<int>(gridDim.x >> 1);
+    item = static_cast<int>(blockIdx.x >> 1) - step;
+    ahead = peek(p, item + step);
+  }
+  // On to the next one.
+  __device__ __forceinline__ bool next(const MlaParams& p) {
+    do {
+      item += step;
+      if (item >= p.items) return false;
+      w = work_of(p, item, ahead);
+      ahead = peek(p, item + step);
+    } while (w.tile1 == w.tile0);
+    return true;
+  }
 };
 // Row of slot s, -1 where there is none.
 __device__ __forceinline__ int32_t row_of(const Work& w, int s) {
@@ -262,197 +341,317 @@ __device__ __forceinline__ void unit_ready(uint32_t full) {
 
 // Brings quantised rows for S, 128 threads: thread = (rows r0 + 16 i, piece of 8
 // entries) of each block.  An absent row is any row's codes with a scale of zero.
+// Two pairs of blocks are in flight: where one has been widened, the one after the
+// next is asked for into the same registers.
 template <int kFmt>
-__device__ __forceinline__ void bring_keys(const Work& w, uint32_t rank, int tid, uint32_t sb, uint32_t* err) {
+__device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7;
   const uint32_t dst0 = sb + kOffK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 16 apart: the same swizzle
   const int own = static_cast<int>(rank) * 64;
   const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
-  // the rows two tiles ahead into L2: lines of 128 bytes, two threads a row
-  auto prefetch = [&](int tile) {
-    if (tile >= w.tile1) return;
-    const int32_t id = row_of(w, tile * kTile + own + (tid >> 1));
-    if (id < 0) return;
-    const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow + (tid & 1) * 128;
-#pragma unroll
-    for (int o = 0; o < kRow; o += 256)
-      if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o);
-  };
-  int32_t id[4];
-  const uint8_t* src[4];
-  bool here[4];
-  auto load_ids = [&](int tile) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) id[i] = tile < w.tile1 ? row_of(w, tile * kTile + own + r0 + 16 * i) : -1;
-  };
-  auto point = [&] {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      here[i] = id[i] >= 0;
-      src[i] = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;
-    }
-  };
-  uint2 cur[8];
-  uint32_t scale[4];
-  auto load_pair = [&](int u, uint2* c, uint32_t* s) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i] = 0u;
-      if (here[i]) s[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i] + kv_code_bytes(kFmt) + 4 * u));
-#pragma unroll
-      for (int x = 0; x < 2; ++x) c[x * 4 + i] = load_code<kFmt>(src[i], u * 128 + x * 64 + piece * 8);
-    }
-  };
-  prefetch(w.tile0);
-  prefetch(w.tile0 + 1);
-  load_ids(w.tile0);
-  point();
-  load_pair(0, cur, scale);
-  load_ids(w.tile0 + 1);
+  uint32_t* err = p.a.err;
   uint32_t parity = 1;
-  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u) {
-    prefetch(tile + 2);
-    uint4 rope[4];
+  for (Items it(p); it.next(p);) {
+    const Work& w = it.w;
+    // the rows two tiles ahead into L2: lines of 128 bytes, two threads a row
+    auto prefetch = [&](int tile) {
+      if (tile >= w.tile1) return;
+      const int32_t id = row_of(w, tile * kTile + own + (tid >> 1));
+      if (id < 0) return;
+      const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow + (tid & 1) * 128;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rope[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (here[i]) rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
-    }
-#pragma unroll 1
-    for (int u = 0; u < 4; ++u) {
-      uint2 next[8];
-      uint32_t nscale[4];
-      if (u == 3) point();
-      load_pair((u + 1) & 3, next, nscale);
-      if (!wait_warp(sb, sb + kKEmpty + 8 * u, parity, err)) return;
+      for (int o = 0; o < kRow; o += 256)
+        if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o);
+    };
+    int32_t id[4];
+    const uint8_t* src[4];
+    bool here[4];
+    auto load_ids = [&](int tile) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = tile * kTile + own + r0 + 16 * i;
+        id[i] = tile < w.tile1 && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
+      }
+    };
+    auto point = [&] {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(err, MISA_DEVERR_BAD_INDEX);
+        here[i] = id[i] >= 0 && id[i] < w.L;
+        src[i] = w.base + static_cast<int64_t>(here[i] ? id[i] : 0) * kRow;
+      }
+    };
+    struct Pair {
+      uint2 code[8];
+      uint32_t scale[4];
+    };
+    auto load_pair = [&](int u, Pair& c) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c.scale[i] = 0u;
+        if (here[i]) c.scale[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i] + kv_code_bytes(kFmt) + 4 * u));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) c.code[x * 4 + i] = load_code<kFmt>(src[i], u * 128 + x * 64 + piece * 8);
+      }
+    };
+    auto write_pair = [&](int u, const Pair& c) {
+      if (!wait_warp(sb + kKEmpty + 8 * u, parity, err)) return false;
       const uint32_t dst = dst0 + u * 2 * kBlockBytes;
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           st_shared16(dst + x * kBlockBytes + i * 2048,
-                      kv_decode8<kFmt>(cur[x * 4 + i].x, cur[x * 4 + i].y, kv_scale(__byte_perm(scale[i], 0u, sel + 2 * x))));
+                      kv_decode8<kFmt>(c.code[x * 4 + i].x, c.code[x * 4 + i].y,
+                                       kv_scale(__byte_perm(c.scale[i], 0u, sel + 2 * x))));
       unit_ready(sb + kKFull + 8 * u);
+      return true;
+    };
+    Pair even, odd;
+    load_ids(w.tile0);
+    point();
+    load_pair(0, even);
+    load_pair(1, odd);
+    prefetch(w.tile0 + 1);
+    for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u) {
+      const bool more = tile + 1 < w.tile1;
+      prefetch(tile + 2);
+      load_ids(tile + 1);
+      uint4 rope[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cur[j] = next[j];
+      for (int i = 0; i < 4; ++i) {
+        rope[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (here[i]) rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
+      }
+#pragma unroll 1
+      for (int u = 0; u < 4; u += 2) {
+        if (!write_pair(u, even)) return;
+        if (u == 2) point();
+        if (u == 0 || more) load_pair(u ^ 2, even);
+        if (!write_pair(u + 1, odd)) return;
+        if (u == 0 || more) load_pair((u ^ 2) + 1, odd);
+      }
+      if (!wait_warp(sb + kKEmpty + 8 * 4, parity, err)) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) scale[i] = nscale[i];
+      for (int i = 0; i < 4; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 2048, rope[i]);
+      unit_ready(sb + kKFull + 8 * 4);
     }
-    load_ids(tile + 2);
-    if (!wait_warp(sb, sb + kKEmpty + 8 * 4, parity, err)) return;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 2048, rope[i]);
-    unit_ready(sb + kKFull + 8 * 4);
   }
 }
 
-// Brings quantised rows for O, 128 threads: entries [256 rank, 256 rank + 256) of 32 rows a unit.
+// Brings quantised rows for O, 128 threads: entries [256 rank, 256 rank + 256) of 32
+// rows a unit, two units in flight.
 template <int kFmt>
-__device__ __forceinline__ void bring_values(const Work& w, uint32_t rank, int tid, uint32_t sb, uint32_t* err) {
+__device__ __forceinline__ void bring_values(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7;
   const uint32_t dst0 = sb + kOffV + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
   const uint32_t sel = 0x4440u | (piece >> 2);
-  int32_t id[2];
-  auto load_ids = [&](int unit) {   // unit: counted over the tiles
+  uint32_t parity = 1;
+  for (Items it(p); it.next(p);) {
+    const Work& w = it.w;
+    const int end = w.tile1 * kVUnits;   // units are counted over the tiles
+    int32_t id[2];
+    auto load_ids = [&](int unit) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) id[i] = unit < w.tile1 * kVUnits ? row_of(w, unit * 32 + r0 + 16 * i) : -1;
-  };
-  uint2 cur[8], scale[2];
-  auto load_unit = [&](uint2* c, uint2* s) {
+      for (int i = 0; i < 2; ++i) id[i] = unit < end ? row_of(w, unit * 32 + r0 + 16 * i) : -1;
+    };
+    struct Unit {
+      uint2 code[8], scale[2];
+    };
+    auto load_unit = [&](Unit& c) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint8_t* src = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;
-      s[i] = make_uint2(0u, 0u);
-      if (id[i] >= 0) s[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* src = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;
+        c.scale[i] = make_uint2(0u, 0u);
+        if (id[i] >= 0) c.scale[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
 #pragma unroll
-      for (int a = 0; a < 4; ++a) c[i * 4 + a] = load_code<kFmt>(src, static_cast<int>(rank) * 256 + a * 64 + piece * 8);
-    }
-  };
-  int unit = w.tile0 * kVUnits;
-  load_ids(unit);
-  load_unit(cur, scale);
-  load_ids(unit + 1);
-  const int first = unit;
-#pragma unroll 1
-  for (; unit < w.tile1 * kVUnits; ++unit) {
-    const int g = unit & (kVUnits - 1);
-    uint2 next[8], nscale[2];
-    load_unit(next, nscale);
+        for (int a = 0; a < 4; ++a) c.code[i * 4 + a] = load_code<kFmt>(src, static_cast<int>(rank) * 256 + a * 64 + piece * 8);
+      }
+    };
+    auto write_unit = [&](int g, const Unit& c) {
+      if (!wait_warp(sb + kVEmpty + 8 * g, parity, p.a.err)) return false;
+      const uint32_t dst = dst0 + g * kVUnitBytes;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+          st_shared16(dst + a * kVAtom + i * 2048,
+                      kv_decode8<kFmt>(c.code[i * 4 + a].x, c.code[i * 4 + a].y,
+                                       kv_scale(__byte_perm(a < 2 ? c.scale[i].x : c.scale[i].y, 0u, sel + 2 * (a & 1)))));
+      unit_ready(sb + kVFull + 8 * g);
+      return true;
+    };
+    Unit even, odd;
+    int unit = w.tile0 * kVUnits;
+    load_ids(unit);
+    load_unit(even);
+    load_ids(unit + 1);
+    load_unit(odd);
     load_ids(unit + 2);
-    if (!wait_warp(sb, sb + kVEmpty + 8 * g, (((unit - first) >> 2) & 1) ^ 1u, err)) return;
-    const uint32_t dst = dst0 + g * kVUnitBytes;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-        st_shared16(dst + a * kVAtom + i * 2048,
-                    kv_decode8<kFmt>(cur[i * 4 + a].x, cur[i * 4 + a].y,
-                                     kv_scale(__byte_perm(a < 2 ? scale[i].x : scale[i].y, 0u, sel + 2 * (a & 1)))));
-    unit_ready(sb + kVFull + 8 * g);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cur[j] = next[j];
-    scale[0] = nscale[0];
-    scale[1] = nscale[1];
+#pragma unroll 1
+    for (; unit < end; unit += 2) {
+      const int g = unit & (kVUnits - 1);
+      if (!write_unit(g, even)) return;
+      if (unit + 2 < end) load_unit(even);
+      load_ids(unit + 3);
+      if (!write_unit(g + 1, odd)) return;
+      if (unit + 3 < end) load_unit(odd);
+      load_ids(unit + 4);
+      if (g) parity ^= 1u;
+    }
   }
 }
 
 // Brings bf16 rows by TMA: one thread asks for those of S and one for those of O,
 // and a warp each passes on what has landed.  Rows behind the prefix are cleared in
 // O's operand: P is 0 there, but 0 times a stale NaN is not.
-__device__ __forceinline__ void ask_keys(const Work& w, uint32_t rank, const CUtensorMap* map, uint32_t sb, uint32_t* err) {
+__device__ __forceinline__ void ask_keys(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
   uint32_t parity = 1;
-  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
-    for (int u = 0; u < kKUnits; ++u) {
-      if (!wait_one(sb, sb + kKEmpty + 8 * u, parity, err)) return;
-      const uint32_t bar = sb + kLanded + 8 * u;
-      const int nb = u < 4 ? 2 : 1;
-      bar_expect(bar, nb * kBlockBytes);
-      for (int x = 0; x < nb; ++x)
-        for (int h = 0; h < 2; ++h)   // 32 rows
-          tma_3d(sb + kOffK + (2 * u + x) * kBlockBytes + h * kVAtom, map, bar, (2 * u + x) * 64,
-                 tile * kTile + static_cast<int>(rank) * 64 + h * 32, w.seq);
+  for (Items it(p); it.next(p);)
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
+      const int row = tile * kTile + static_cast<int>(rank) * 64;
+      for (int u = 0; u < kKUnits; ++u) {
+        if (!wait_one(sb + kKEmpty + 8 * u, parity, p.a.err)) return;
+        const uint32_t bar = sb + kLanded + 8 * u;
+        const int nb = u < 4 ? 2 : 1;
+        bar_expect(bar, nb * kBlockBytes);
+        for (int x = 0; x < nb; ++x)
+          for (int h = 0; h < 2; ++h)   // 32 rows
+            tma_3d(sb + kOffK + (2 * u + x) * kBlockBytes + h * kVAtom, map, bar, (2 * u + x) * 64, row + h * 32, it.w.seq);
+        if (tile + 2 < it.w.tile1)      // the same place two tiles ahead into L2
+          for (int x = 0; x < nb; ++x)
+            for (int h = 0; h < 2; ++h) tma_l2_3d(map, (2 * u + x) * 64, row + 2 * kTile + h * 32, it.w.seq);
+      }
     }
 }
-__device__ __forceinline__ void ask_values(const Work& w, uint32_t rank, const CUtensorMap* map, uint32_t sb, uint32_t* err) {
+__device__ __forceinline__ void ask_values(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
   uint32_t parity = 1;
-  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
-    for (int g = 0; g < kVUnits; ++g) {
-      if (!wait_one(sb, sb + kVEmpty + 8 * g, parity, err)) return;
-      const uint32_t bar = sb + kLanded + 8 * (kKUnits + g);
-      bar_expect(bar, kVUnitBytes);
-      for (int a = 0; a < 4; ++a)
-        tma_3d(sb + kOffV + g * kVUnitBytes + a * kVAtom, map, bar, static_cast<int>(rank) * 256 + a * 64, tile * kTile + g * 32, w.seq);
-    }
+  for (Items it(p); it.next(p);)
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u)
+      for (int g = 0; g < kVUnits; ++g) {
+        if (!wait_one(sb + kVEmpty + 8 * g, parity, p.a.err)) return;
+        const uint32_t bar = sb + kLanded + 8 * (kKUnits + g);
+        bar_expect(bar, kVUnitBytes);
+        for (int a = 0; a < 4; ++a)
+          tma_3d(sb + kOffV + g * kVUnitBytes + a * kVAtom, map, bar, static_cast<int>(rank) * 256 + a * 64,
+                 tile * kTile + g * 32, it.w.seq);
+      }
 }
-__device__ __forceinline__ void pass_keys(const Work& w, uint32_t sb, uint32_t* err) {
+__device__ __forceinline__ void pass_keys(const MlaParams& p, uint32_t sb) {
   uint32_t parity = 0;
-  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
-    for (int u = 0; u < kKUnits; ++u) {
-      if (!wait_one(sb, sb + kLanded + 8 * u, parity, err)) return;
-      arrive_in(sb + kKFull + 8 * u, 0);
-    }
+  for (Items it(p); it.next(p);)
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u)
+      for (int u = 0; u < kKUnits; ++u) {
+        if (!wait_one(sb + kLanded + 8 * u, parity, p.a.err)) return;
+        arrive_in(sb + kKFull + 8 * u, 0);
+      }
 }
-__device__ __forceinline__ void pass_values(const Work& w, int lane, uint32_t sb, uint32_t* err) {
+__device__ __forceinline__ void pass_values(const MlaParams& p, int lane, uint32_t sb) {
   uint32_t parity = 0;
-  for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u)
-    for (int g = 0; g < kVUnits; ++g) {
-      if (!wait_warp(sb, sb + kLanded + 8 * (kKUnits + g), parity, err)) return;
-      const int live = min(max(w.n - tile * kTile - g * 32, 0), 32);   // rows of this unit that exist
-      for (int a = 0; a < 4; ++a)
-        for (int c = live * 8 + lane; c < 32 * 8; c += 32)   // whole rows: the swizzle does not matter
-          st_shared16(sb + kOffV + g * kVUnitBytes + a * kVAtom + c * 16, make_uint4(0u, 0u, 0u, 0u));
-      unit_ready(sb + kVFull + 8 * g);
-    }
+  for (Items it(p); it.next(p);)
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u)
+      for (int g = 0; g < kVUnits; ++g) {
+        if (!wait_warp(sb + kLanded + 8 * (kKUnits + g), parity, p.a.err)) return;
+        const int live = min(max(it.w.n - tile * kTile - g * 32, 0), 32);   // rows of this unit that exist
+        for (int a = 0; a < 4; ++a)
+          for (int c = live * 8 + lane; c < 32 * 8; c += 32)   // whole rows: the swizzle does not matter
+            st_shared16(sb + kOffV + g * kVUnitBytes + a * kVAtom + c * 16, make_uint4(0u, 0u, 0u, 0u));
+        unit_ready(sb + kVFull + 8 * g);
+      }
 }
 
-struct MlaParams {
-  LatentArgs a;
-  int nsplit;
-  float* part_o;     // [T][nsplit][Hq][512] (nsplit > 1)
-  float* part_ml;    // [T][nsplit][Hq][2]: m (log2 units), l
-};
+// Brings the queries of this CTA's heads, an item at a time.
+__device__ __forceinline__ void bring_queries(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
+  uint32_t parity = 0;
+  for (Items it(p); it.next(p); parity ^= 1u) {
+    if (!wait_one(sb + kQEmpty, parity ^ 1u, p.a.err)) return;
+    bar_expect(sb + kQFull, kBlocks * kBlockBytes);
+    for (int b = 0; b < kBlocks; ++b)
+      tma_2d(sb + kOffQ + b * kBlockBytes, map, sb + kQFull, b * 64, it.w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
+    if (!wait_one(sb + kQFull, parity, p.a.err)) return;
+    arrive_in(sb + kQReady, 0);
+  }
+}
+
+// Issues the products of both CTAs, a warp of the first: S of tile n + 1, then
+// O += P V of tile n, over the items.  The warp waits as a whole and one lane issues
+// what a unit allows.
+__device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint32_t sb) {
+  uint32_t* err = p.a.err;
+  const bool leader = elect_one();
+  Items si(p), oi(p);
+  bool s_any = si.next(p), o_any = oi.next(p), ok = true;
+  int s_tile = s_any ? si.w.tile0 : 0, o_tile = s_tile;
+  uint32_t st = 0, ot = 0;              // tiles so far
+  uint32_t s_items = 0, o_items = 0;    // items finished
+  while (ok && o_any) {
+    // S, one tile ahead
+    while (ok && s_any && st < ot + 2) {
+      if (s_tile == si.w.tile0) ok = wait_warp(sb + kQReady, s_items & 1, err);
+      const uint32_t place = st & 1;
+      ok = ok && wait_warp(sb + kSEmpty + 8 * place, ((st >> 1) & 1) ^ 1u, err);
+      const uint32_t d = tmem + kTmemS + place * 64;
+#pragma unroll 1
+      for (uint32_t u = 0; u < kKUnits && ok; ++u) {
+        ok = wait_warp(sb + kKFull + 8 * u, place, err);
+        if (leader && ok) {
+          tc_fence_after();
+          const uint64_t q = sw128_kmajor_desc(sb + kOffQ + u * 2 * kBlockBytes);
+          const uint64_t k = sw128_kmajor_desc(sb + kOffK + u * 2 * kBlockBytes);
+          umma_pair<0, 0>(d, q, k, kIdescS, u);
+          umma_pair<32, 32>(d, q, k, kIdescS, 1);
+          umma_pair<64, 64>(d, q, k, kIdescS, 1);
+          umma_pair<96, 96>(d, q, k, kIdescS, 1);
+          if (u < 4) {
+            umma_pair<kBlockBytes, kBlockBytes>(d, q, k, kIdescS, 1);
+            umma_pair<kBlockBytes + 32, kBlockBytes + 32>(d, q, k, kIdescS, 1);
+            umma_pair<kBlockBytes + 64, kBlockBytes + 64>(d, q, k, kIdescS, 1);
+            umma_pair<kBlockBytes + 96, kBlockBytes + 96>(d, q, k, kIdescS, 1);
+          }
+          commit_pair(sb + kKEmpty + 8 * u);
+        }
+      }
+      if (leader) commit_pair(sb + kSFull + 8 * place);
+      ++st;
+      if (++s_tile == si.w.tile1) {
+        if (leader) commit_pair(sb + kQEmpty);
+        s_any = si.next(p);
+        s_tile = si.w.tile0;
+        ++s_items;
+      }
+    }
+    // O
+    const bool first = o_tile == oi.w.tile0;
+    if (first && o_items) ok = ok && wait_warp(sb + kOEmpty, (o_items - 1) & 1, err);
+    ok = ok && wait_warp(sb + kPFull, ot & 1, err);
+#pragma unroll 1
+    for (uint32_t g = 0; g < kVUnits && ok; ++g) {
+      ok = wait_warp(sb + kVFull + 8 * g, ot & 1, err);
+      if (leader && ok) {
+        tc_fence_after();
+        const uint64_t w = sw128_kmajor_desc(sb + kOffP + (g >> 1) * kBlockBytes + (g & 1) * 64);
+        const uint64_t v = sw128_mnmajor_desc(sb + kOffV + g * kVUnitBytes, kVAtom);
+        const uint32_t add = g || !first;
+        umma_pair<0, 0>(tmem, w, v, kIdescO, add);                        // 16 rows, entries 0 .. 127 of each half
+        umma_pair<0, 2 * kVAtom>(tmem + 128, w, v, kIdescO, add);
+        umma_pair<32, 2048>(tmem, w, v, kIdescO, 1);
+        umma_pair<32, 2 * kVAtom + 2048>(tmem + 128, w, v, kIdescO, 1);
+        commit_pair(sb + kVEmpty + 8 * g);
+      }
+    }
+    if (leader) commit_pair(sb + kPvDone);
+    ++ot;
+    if (++o_tile == oi.w.tile1) {
+      o_any = oi.next(p);
+      o_tile = oi.w.tile0;
+      ++o_items;
+    }
+  }
+  if (leader) commit_pair(sb + kDone);
+  __syncwarp();
+}
 
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
@@ -461,7 +660,6 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
-  const int item = static_cast<int>(blockIdx.x >> 1);
   if (tid == 0) {
     constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 2 : 8;   // arriving warps of both CTAs
     for (int i = 0; i < kKUnits; ++i) { bar_init(sb + kKFull + 8 * i, kWriters); bar_init(sb + kKEmpty + 8 * i, 1); }
@@ -470,10 +668,11 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     for (int i = 0; i < 2; ++i) { bar_init(sb + kSFull + 8 * i, 1); bar_init(sb + kSEmpty + 8 * i, 8); }
     bar_init(sb + kPFull, 8);
     bar_init(sb + kPvDone, 1);
+    bar_init(sb + kOEmpty, 8);
+    bar_init(sb + kQEmpty, 1);
     bar_init(sb + kQFull, 1);
     bar_init(sb + kQReady, 2);
     bar_init(sb + kDone, 1);
-    st_shared(sb + kOffAbort, 0u);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -494,114 +693,34 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 
   const LatentArgs& a = p.a;
   uint32_t* err = a.err;
-  Work w;
-  w.t = item / p.nsplit;
-  const int split = item - w.t * p.nsplit;
-  w.L = a.L;
-  w.idx = a.idx ? a.idx + static_cast<int64_t>(w.t) * a.idx_stride : nullptr;
-  int64_t n = a.idx ? a.k : min(static_cast<int64_t>(a.prefix_len[w.t]), a.L);
-  int64_t seq = a.seq_of[w.t];
-  if (seq < 0 || seq >= a.nseq) {
-    if (tid == 0) record_error(err, MISA_DEVERR_BAD_SEQ);
-    seq = 0;
-    n = 0;
-  }
-  w.n = static_cast<int>(max(n, static_cast<int64_t>(0)));
-  w.seq = static_cast<int>(seq);
-  w.base = static_cast<const uint8_t*>(a.cache) + seq * a.seq_stride;
-  const int tiles = (w.n + kTile - 1) / kTile;
-  const int share = (tiles + p.nsplit - 1) / p.nsplit;
-  w.tile0 = min(split * share, tiles);
-  w.tile1 = min(w.tile0 + share, tiles);
-  const int ntiles = w.tile1 - w.tile0;
-
-  if (warp >= kVWarp0) {
-    if (ntiles > 0) {
-      if constexpr (kFmt == MISA_KV_BF16) {
-        if (warp == kVWarp0 && elect_one()) ask_values(w, rank, &row_map, sb, err);
-        if (warp == kVWarp0 + 1) pass_values(w, lane, sb, err);
-      } else {
-        bring_values<kFmt>(w, rank, tid - kVWarp0 * 32, sb, err);
-      }
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == kMmaWarp) {
+      if (rank == 0) multiply(p, tmem, sb);
+      wait_all(sb, err);   // nothing reads this CTA's memory any more
+      __syncwarp();
+    } else if (warp == kQWarp) {
+      if (elect_one()) bring_queries(p, rank, &q_map, sb);
+      __syncwarp();
+    }
+  } else if (warp >= kVWarp0) {
+    if constexpr (kFmt == MISA_KV_BF16) {
+      if (warp == kVWarp0 && elect_one()) ask_values(p, rank, &row_map, sb);
+      if (warp == kVWarp0 + 1) pass_values(p, lane, sb);
+      __syncwarp();
+    } else {
+      bring_values<kFmt>(p, rank, tid - kVWarp0 * 32, sb);
     }
   } else if (warp >= kKWarp0) {
-    if (ntiles > 0) {
-      if constexpr (kFmt == MISA_KV_BF16) {
-        if (warp == kKWarp0 && elect_one()) ask_keys(w, rank, &row_map, sb, err);
-        if (warp == kKWarp0 + 1 && elect_one()) pass_keys(w, sb, err);
-      } else {
-        // ids that name no row: each slot is looked at by one thread of the first CTA
-        if (w.idx && rank == 0) {
-          for (int s = w.tile0 * kTile + tid - kKWarp0 * 32; s < min(w.n, w.tile1 * kTile); s += 128)
-            if (w.idx[s] < -1 || w.idx[s] >= w.L) record_error(err, MISA_DEVERR_BAD_INDEX);
-        }
-        bring_keys<kFmt>(w, rank, tid - kKWarp0 * 32, sb, err);
-      }
+    if constexpr (kFmt == MISA_KV_BF16) {
+      if (warp == kKWarp0 && elect_one()) ask_keys(p, rank, &row_map, sb);
+      if (warp == kKWarp0 + 1 && elect_one()) pass_keys(p, sb);
+      __syncwarp();
+    } else {
+      bring_keys<kFmt>(p, rank, tid - kKWarp0 * 32, sb);
     }
-  } else if (warp == kMmaWarp) {
-    if (ntiles > 0 && elect_one()) {
-      bar_expect(sb + kQFull, kBlocks * kBlockBytes);
-      for (int b = 0; b < kBlocks; ++b)
-        tma_2d(sb + kOffQ + b * kBlockBytes, &q_map, sb + kQFull, b * 64, w.t * a.Hq + static_cast<int>(rank) * kHeads);
-      bool ok = wait_one(sb, sb + kQFull, 0, err);
-      if (ok) arrive_in(sb + kQReady, 0);
-      if (rank == 0) {
-        // Two rows of work, S of tile s unit by unit and O += P V of tile o unit by
-        // unit; whatever has its operands next is issued, O first.
-        ok = ok && wait_one(sb, sb + kQReady, 0, err);
-        int s_tile = 0, s_unit = 0, o_tile = 0, o_unit = 0;
-        Patience left = {0, 0};
-        while (ok && o_tile < ntiles) {
-          if (o_tile < s_tile && (o_unit || test_phase(sb + kPFull, o_tile & 1)) &&
-              test_phase(sb + kVFull + 8 * o_unit, o_tile & 1)) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const int step = o_unit * 2 + kk;   // 16 rows
-              const uint64_t ad = sw128_kmajor_desc(sb + kOffP + (step >> 2) * kBlockBytes + (step & 3) * 32);
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                umma_pair(tmem + j * 128, ad,
-                          sw128_mnmajor_desc(sb + kOffV + o_unit * kVUnitBytes + j * 2 * kVAtom + kk * 2048, kVAtom), kIdescO,
-                          (o_tile | step) ? 1u : 0u);
-            }
-            commit_pair(sb + kVEmpty + 8 * o_unit);
-            if (++o_unit == kVUnits) {
-              commit_pair(sb + kPvDone);
-              o_unit = 0;
-              ++o_tile;
-            }
-            left.spins = 0;
-          } else if (s_tile < ntiles && (s_unit || test_phase(sb + kSEmpty + 8 * (s_tile & 1), ((s_tile >> 1) & 1) ^ 1u)) &&
-                     test_phase(sb + kKFull + 8 * s_unit, s_tile & 1)) {
-            tc_fence_after();
-            const uint32_t d = tmem + kTmemS + (s_tile & 1) * 64;
-#pragma unroll 1
-            for (int x = 0; x < (s_unit < 4 ? 2 : 1); ++x) {
-              const uint32_t at = (2 * s_unit + x) * kBlockBytes;
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_pair(d, sw128_kmajor_desc(sb + kOffQ + at + kk * 32), sw128_kmajor_desc(sb + kOffK + at + kk * 32),
-                          kIdescS, (s_unit | x | kk) ? 1u : 0u);
-            }
-            commit_pair(sb + kKEmpty + 8 * s_unit);
-            if (++s_unit == kKUnits) {
-              commit_pair(sb + kSFull + 8 * (s_tile & 1));
-              s_unit = 0;
-              ++s_tile;
-            }
-            left.spins = 0;
-          } else {
-            ok = left.more(sb, err);
-          }
-        }
-        commit_pair(sb + kDone);
-      }
-      // both: nothing reads this CTA's memory any more
-      if (!wait_one(sb, sb + kDone, 0, err)) ok = false;
-    }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ------------------------------------------------------------ softmax and output
     const int half = warp >> 1;                     // rows [64 half, 64 half + 64) of a tile, entries 256 half .. of O
     const int hl = (warp & 1) * 32 + lane;          // head of this CTA
@@ -609,36 +728,43 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float kNegInf = -__int_as_float(0x7f800000);
     const float c = fmaxf(a.scale_log2, 1.2e-38f);   // a scale of 0 weighs all rows alike; -inf stays -inf
-    float m = kNegInf, l = 0.f;
     bool ok = true;
-    for (int i = 0; i < ntiles; ++i) {
+    uint32_t st = 0;    // tiles so far
+    Peek ahead = peek(p, static_cast<int>(blockIdx.x >> 1));
+    for (int item = static_cast<int>(blockIdx.x >> 1); item < p.items; item += static_cast<int>(gridDim.x >> 1)) {
+    const Work w = work_of(p, item, ahead);
+    if (tid == 0 && rank == 0 && (ahead.seq < 0 || ahead.seq >= a.nseq)) record_error(err, MISA_DEVERR_BAD_SEQ);
+    ahead = peek(p, item + static_cast<int>(gridDim.x >> 1));
+    const int ntiles = w.tile1 - w.tile0;
+    float m = kNegInf, l = 0.f;
+    for (int i = 0; i < ntiles; ++i, ++st) {
       // rows of this half that exist: two words, the same in the whole warp
       uint32_t live[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         live[j] = __ballot_sync(0xffffffffu, row_of(w, (w.tile0 + i) * kTile + half * 64 + j * 32 + lane) >= 0);
       // a wait that gave up ends the work, not the loop: the warps' barriers stay paired
-      ok = ok && wait_warp(sb, sb + kSFull + 8 * (i & 1), (i >> 1) & 1, err);
+      ok = ok && wait_warp(sb + kSFull + 8 * (st & 1), (st >> 1) & 1, err);
       uint32_t s[64];
+      float mx = kNegInf;
       if (ok) {
         tc_fence_after();
-        tmem_ld32(t_lane + kTmemS + (i & 1) * 64, s);
-        tmem_ld32(t_lane + kTmemS + (i & 1) * 64 + 32, s + 32);
+        tmem_ld32(t_lane + kTmemS + (st & 1) * 64, s);
+        tmem_ld32(t_lane + kTmemS + (st & 1) * 64 + 32, s + 32);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_in(sb + kSEmpty + 8 * (i & 1), 0);
-      }
-      if ((live[0] & live[1]) != 0xffffffffu) {
+        if (lane == 0) arrive_in(sb + kSEmpty + 8 * (st & 1), 0);
+        if ((live[0] & live[1]) != 0xffffffffu) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (!((live[j >> 5] >> (j & 31)) & 1u)) s[j] = 0xff800000u;
-      }
-      float mx = __uint_as_float(s[0]);
+          for (int j = 0; j < 64; ++j)
+            if (!((live[j >> 5] >> (j & 31)) & 1u)) s[j] = 0xff800000u;
+        }
 #pragma unroll
-      for (int j = 1; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
+        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
+      }
       // the other half of the tile's rows for the same head
-      const uint32_t red = sb + kOffRed + (i & 1) * 512;
+      const uint32_t red = sb + kOffRed + (st & 1) * 512;
       st_shared(red + tid * 4, __float_as_uint(mx));
       named_bar_sync(1, 128);
       mx = fmaxf(mx, __uint_as_float(ld_shared(red + (tid ^ 64) * 4))) * c;
@@ -658,7 +784,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         s[j >> 1] = pack_bf16(x, y);
       }
       l += l0 + l1;
-      if (i > 0) ok = ok && wait_warp(sb, sb + kPvDone, (i - 1) & 1, err);
+      if (i > 0) ok = ok && wait_warp(sb + kPvDone, (st - 1) & 1, err);
       if (!ok) continue;
       if (i > 0) {
         tc_fence_after();
@@ -685,60 +811,82 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       __syncwarp();
       if (lane == 0) arrive_in(sb + kPFull, 0);
     }
-    // both halves' sums; a barrier apart from the last tile's exchange
-    named_bar_sync(1, 128);
-    st_shared(sb + kOffRed + tid * 4, __float_as_uint(l));
-    named_bar_sync(1, 128);
-    l += __uint_as_float(ld_shared(sb + kOffRed + (tid ^ 64) * 4));
-    if (ntiles > 0) {
-      ok = ok && wait_warp(sb, sb + kPvDone, (ntiles - 1) & 1, err);
+    if (ntiles > 0) {   // both halves' sums
+      st_shared(sb + kOffRed + 1024 + tid * 4, __float_as_uint(l));
+      named_bar_sync(1, 128);
+      l += __uint_as_float(ld_shared(sb + kOffRed + 1024 + (tid ^ 64) * 4));
+      ok = ok && wait_warp(sb + kPvDone, (st - 1) & 1, err);
       tc_fence_after();
     }
-    const int64_t row = p.nsplit > 1 ? (static_cast<int64_t>(w.t) * p.nsplit + split) * a.Hq + h
-                                     : static_cast<int64_t>(w.t) * a.Hq + h;
+    // Output by 128 bytes a row: each warp turns its 32 heads' pieces round in its
+    // 4 KB of P (free until the next tile), so that eight lanes store a row's piece.
+    // (Stored straight from TMEM's lanes, each to a row of its own, an item's output
+    // took 4 us.)
     const bool any = l > 0.f || l != l;
-    if (p.nsplit > 1) {
-      if (h < a.Hq && half == 0) {
-        p.part_ml[row * 2] = any ? m : kNegInf;
-        p.part_ml[row * 2 + 1] = l;
+    const int64_t row0 = (p.nsplit > 1 ? static_cast<int64_t>(w.t) * p.nsplit + w.split : static_cast<int64_t>(w.t)) * a.Hq;
+    const int h0 = static_cast<int>(rank) * kHeads + (warp & 1) * 32;   // first head of the warp
+    if (h < a.Hq && half == 0) {
+      if (p.nsplit > 1)
+        *reinterpret_cast<float2*>(p.part_ml + (row0 + h) * 2) = make_float2(any ? m : kNegInf, l);
+      else if (a.lse)
+        a.lse[row0 + h] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+    }
+    const uint32_t turn = sb + kOffP + warp * 4096;
+    auto turned = [&](uint8_t* out, int64_t row_bytes) {   // out: where the first head's piece goes
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = j * 4 + (lane >> 3);
+        if (h0 + r < a.Hq)
+          *reinterpret_cast<uint4*>(out + r * row_bytes + (lane & 7) * 16) =
+              ld_shared16(turn + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
       }
-      if (ntiles > 0 && ok) {
+      __syncwarp();
+    };
+    const bool have = ntiles > 0 && ok;
+    if (p.nsplit > 1) {
+      uint8_t* out = reinterpret_cast<uint8_t*>(p.part_o + (row0 + h0) * kDv + half * 256);
+      if (have) {
 #pragma unroll 1
         for (int o = 0; o < 256; o += 32) {
           uint32_t v[32];
           tmem_ld32(t_lane + o, v);
           tmem_wait_ld();
-          if (h < a.Hq) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + row * kDv + half * 256 + o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                   __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-          }
+          for (int j = 0; j < 8; ++j)
+            st_shared16(turn + lane * 128 + ((j ^ (lane & 7)) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+          turned(out + o * 4, kDv * 4);
         }
       }
     } else {
       const float inv = any ? 1.f / l : 0.f;
-      if (a.lse && h < a.Hq && half == 0) a.lse[row] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+      uint8_t* out = reinterpret_cast<uint8_t*>(a.out + (row0 + h0) * kDv + half * 256);
 #pragma unroll 1
-      for (int o = 0; o < 256; o += 32) {
-        uint32_t v[32];
-        if (ntiles > 0 && ok) {
-          tmem_ld32(t_lane + o, v);
-          tmem_wait_ld();
-        }
-        if (h < a.Hq) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + row * kDv + half * 256 + o);
+      for (int o = 0; o < 256; o += 64) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t v[32];
+          if (have) {
+            tmem_ld32(t_lane + o + q * 32, v);
+            tmem_wait_ld();
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t q[4];
+            uint32_t x[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              q[u] = any ? pack_bf16(__uint_as_float(v[8 * j + 2 * u]) * inv, __uint_as_float(v[8 * j + 2 * u + 1]) * inv) : 0u;
-            dst[j] = make_uint4(q[0], q[1], q[2], q[3]);
+              x[u] = have && any ? pack_bf16(__uint_as_float(v[8 * j + 2 * u]) * inv, __uint_as_float(v[8 * j + 2 * u + 1]) * inv) : 0u;
+            st_shared16(turn + lane * 128 + (((q * 4 + j) ^ (lane & 7)) << 4), make_uint4(x[0], x[1], x[2], x[3]));
           }
         }
+        turned(out + o * 2, kDv * 2);
       }
+    }
+    if (ntiles > 0 && ok) {   // O has been read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_in(sb + kOEmpty, 0);
+    }
     }
   }
 
@@ -793,17 +941,17 @@ latent_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
 // Clusters that run at once on the 148 SMs of a B200.
 constexpr int kSlots = 74;
 
-// How many clusters share a query's rows.  A cluster's time is its tiles and about
-// three tiles' worth of set-up and output, a join costs about two more; the split
-// that makes the waves of all clusters shortest is taken.
+// How many items share a query's rows.  An item takes its tiles and about one and
+// a half tiles' worth of queries and output, a join about three more at the end;
+// the split that makes the busiest cluster's list shortest is taken.
 int pick_splits(int T, int64_t n) {
   const int64_t tiles = (n + kTile - 1) / kTile;
   int best = 1;
   int64_t best_cost = -1;
   for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-    if (s > 1 && static_cast<int64_t>(T) * s > 2 * kSlots) break;
-    const int64_t waves = (static_cast<int64_t>(T) * s + kSlots - 1) / kSlots;
-    const int64_t cost = waves * ((tiles + s - 1) / s + 3) + (s > 1 ? 2 : 0);
+    if (s > 1 && static_cast<int64_t>(T) * s > 4 * kSlots) break;
+    const int64_t rounds = (static_cast<int64_t>(T) * s + kSlots - 1) / kSlots;
+    const int64_t cost = rounds * (2 * ((tiles + s - 1) / s) + 3) + (s > 1 ? 6 : 0);
     if (best_cost < 0 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -838,7 +986,10 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
                                      : latent_mla_kernel<MISA_KV_MX4>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(a.T) * p.nsplit * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
+  p.items = a.T * p.nsplit;
+  p.by_nsplit = p.nsplit > 1 ? static_cast<uint32_t>(((1ull << 32) + p.nsplit - 1) / p.nsplit) : 0u;
+  const int clusters = p.items < kSlots ? p.items : kSlots;
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * a.Hq), dim3(128), 0, stream, 0,
                     static_cast<const float*>(p.part_o), static_cast<const float*>(p.part_ml), a.Hq, p.nsplit, a.out, a.lse);
