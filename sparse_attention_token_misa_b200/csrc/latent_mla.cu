@@ -40,8 +40,9 @@
 // items, whose partial sums a second kernel joins in a fixed order.
 //
 // Roles (512 threads a CTA, by warpgroups): warps 0-3 softmax and output (a lane of
-// TMEM each), warps 4-7 bring the rows of S, warps 8-11 those of O, warp 12 has TMEM
-// and, in the first CTA, issues the MMAs, warp 13 brings the queries.  The softmax
+// TMEM each), warps 4-7 bring quantised rows for S, warps 8-11 for O, warp 12 has
+// TMEM and, in the first CTA, issues the MMAs, warp 13 asks for what comes by TMA and
+// warp 14 passes on what has landed.  The softmax
 // holds a tile's 64 scores a lane and more, so the last warpgroup gives it 48 of its
 // registers a thread.  Shared memory is addressed from one 32-bit base: with a
 // pointer a barrier the kernel spilled, and what shared memory leaves of L1 does
@@ -73,8 +74,9 @@ constexpr uint32_t kKFull = kOffBar;              // [5] first CTA: unit brought
 constexpr uint32_t kKEmpty = kKFull + 8 * kKUnits;   // [5] multiplied
 constexpr uint32_t kVFull = kKEmpty + 8 * kKUnits;   // [4] first CTA
 constexpr uint32_t kVEmpty = kVFull + 8 * kVUnits;   // [4]
-constexpr uint32_t kLanded = kVEmpty + 8 * kVUnits;  // [9] bf16: TMA done, S units then O units
-constexpr uint32_t kSFull = kLanded + 8 * (kKUnits + kVUnits);   // [2] S complete
+constexpr uint32_t kKLanded = kVEmpty + 8 * kVUnits;  // [5] bf16: TMA done
+constexpr uint32_t kVLanded = kKLanded + 8 * kKUnits; // [4]
+constexpr uint32_t kSFull = kVLanded + 8 * kVUnits;   // [2] S complete
 constexpr uint32_t kSEmpty = kSFull + 16;         // [2] first CTA: S read by both
 constexpr uint32_t kPFull = kSEmpty + 16;         // first CTA: P written (and O scaled) by both
 constexpr uint32_t kPvDone = kPFull + 8;          // O += P V complete
@@ -87,7 +89,7 @@ constexpr uint32_t kOffTmem = kDone + 8;
 constexpr uint32_t kOffRed = (kOffTmem + 8 + 15) / 16 * 16;   // [3][128] floats
 constexpr int kSmemBytes = kOffRed + 3 * 128 * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kQWarp = 13, kThreads = 16 * 32;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kThreads = 16 * 32;
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 64 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -341,8 +343,8 @@ __device__ __forceinline__ void unit_ready(uint32_t full) {
 
 // Brings quantised rows for S, 128 threads: thread = (rows r0 + 16 i, piece of 8
 // entries) of each block.  An absent row is any row's codes with a scale of zero.
-// Two pairs of blocks are in flight: where one has been widened, the one after the
-// next is asked for into the same registers.
+// Where a piece has been widened, the same piece of the next unit is asked for into
+// its registers.
 template <int kFmt>
 __device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
@@ -354,19 +356,12 @@ __device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, in
   uint32_t parity = 1;
   for (Items it(p); it.next(p);) {
     const Work& w = it.w;
-    // the rows two tiles ahead into L2: lines of 128 bytes, two threads a row
-    auto prefetch = [&](int tile) {
-      if (tile >= w.tile1) return;
-      const int32_t id = row_of(w, tile * kTile + own + (tid >> 1));
-      if (id < 0) return;
-      const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow + (tid & 1) * 128;
-#pragma unroll
-      for (int o = 0; o < kRow; o += 256)
-        if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o);
-    };
     int32_t id[4];
     const uint8_t* src[4];
     bool here[4];
+    uint2 code[8];
+    uint32_t scale[4];
+    uint4 rope[4];
     auto load_ids = [&](int tile) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -374,74 +369,64 @@ __device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, in
         id[i] = tile < w.tile1 && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
       }
     };
-    auto point = [&] {
+    load_ids(w.tile0);
+    // Units of the tiles, four pairs each; the first turn only asks for unit 0.
+#pragma unroll 1
+    for (int unit = 4 * w.tile0 - 1; unit < 4 * w.tile1; ++unit) {
+      const int tile = unit >> 2, u = unit & 3, next = (u + 1) & 3;
+      const bool real = unit >= 4 * w.tile0;
+      if (u == 3) {   // on to the rows of the next tile
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(err, MISA_DEVERR_BAD_INDEX);
-        here[i] = id[i] >= 0 && id[i] < w.L;
-        src[i] = w.base + static_cast<int64_t>(here[i] ? id[i] : 0) * kRow;
+        for (int i = 0; i < 4; ++i) {
+          if (piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(err, MISA_DEVERR_BAD_INDEX);
+          here[i] = id[i] >= 0 && id[i] < w.L;
+          src[i] = w.base + static_cast<int64_t>(here[i] ? id[i] : 0) * kRow;
+        }
+        load_ids(tile + 2);
+        // those two tiles ahead into L2: lines of 128 bytes, two threads a row
+        const int far = (tile + 3) * kTile + own + (tid >> 1);
+        if (tile + 3 < w.tile1 && far < w.n) {
+          const int32_t fid = row_of(w, far);
+          const uint8_t* row = w.base + static_cast<int64_t>(max(fid, 0)) * kRow + (tid & 1) * 128;
+#pragma unroll
+          for (int o = 0; o < kRow; o += 256)
+            if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o);
+        }
       }
-    };
-    struct Pair {
-      uint2 code[8];
-      uint32_t scale[4];
-    };
-    auto load_pair = [&](int u, Pair& c) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c.scale[i] = 0u;
-        if (here[i]) c.scale[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i] + kv_code_bytes(kFmt) + 4 * u));
-#pragma unroll
-        for (int x = 0; x < 2; ++x) c.code[x * 4 + i] = load_code<kFmt>(src[i], u * 128 + x * 64 + piece * 8);
-      }
-    };
-    auto write_pair = [&](int u, const Pair& c) {
-      if (!wait_warp(sb + kKEmpty + 8 * u, parity, err)) return false;
+      if (real && !wait_warp(sb + kKEmpty + 8 * u, parity, err)) return;
       const uint32_t dst = dst0 + u * 2 * kBlockBytes;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          st_shared16(dst + x * kBlockBytes + i * 2048,
-                      kv_decode8<kFmt>(c.code[x * 4 + i].x, c.code[x * 4 + i].y,
-                                       kv_scale(__byte_perm(c.scale[i], 0u, sel + 2 * x))));
-      unit_ready(sb + kKFull + 8 * u);
-      return true;
-    };
-    Pair even, odd;
-    load_ids(w.tile0);
-    point();
-    load_pair(0, even);
-    load_pair(1, odd);
-    prefetch(w.tile0 + 1);
-    for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u) {
-      const bool more = tile + 1 < w.tile1;
-      prefetch(tile + 2);
-      load_ids(tile + 1);
-      uint4 rope[4];
-#pragma unroll
       for (int i = 0; i < 4; ++i) {
-        rope[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (here[i]) rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
-      }
-#pragma unroll 1
-      for (int u = 0; u < 4; u += 2) {
-        if (!write_pair(u, even)) return;
-        if (u == 2) point();
-        if (u == 0 || more) load_pair(u ^ 2, even);
-        if (!write_pair(u + 1, odd)) return;
-        if (u == 0 || more) load_pair((u ^ 2) + 1, odd);
-      }
-      if (!wait_warp(sb + kKEmpty + 8 * 4, parity, err)) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 2048, rope[i]);
-      unit_ready(sb + kKFull + 8 * 4);
+        for (int x = 0; x < 2; ++x) {
+          const uint4 y = kv_decode8<kFmt>(code[2 * i + x].x, code[2 * i + x].y, kv_scale(__byte_perm(scale[i], 0u, sel + 2 * x)));
+          if (real) st_shared16(dst + x * kBlockBytes + i * 2048, y);
+          code[2 * i + x] = load_code<kFmt>(src[i], next * 128 + x * 64 + piece * 8);
+        }
+        scale[i] = 0u;
+        if (here[i]) scale[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i] + kv_code_bytes(kFmt) + 4 * next));
+      }
+      if (real) unit_ready(sb + kKFull + 8 * u);
+      if (u == 3) {   // the rotary block of this tile, and the next one's asked for
+        if (real) {
+          if (!wait_warp(sb + kKEmpty + 8 * 4, parity, err)) return;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 2048, rope[i]);
+          unit_ready(sb + kKFull + 8 * 4);
+          parity ^= 1u;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          rope[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (here[i]) rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
+        }
+      }
     }
   }
 }
 
 // Brings quantised rows for O, 128 threads: entries [256 rank, 256 rank + 256) of 32
-// rows a unit, two units in flight.
+// rows a unit.
 template <int kFmt>
 __device__ __forceinline__ void bring_values(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
@@ -453,126 +438,126 @@ __device__ __forceinline__ void bring_values(const MlaParams& p, uint32_t rank, 
     const Work& w = it.w;
     const int end = w.tile1 * kVUnits;   // units are counted over the tiles
     int32_t id[2];
+    uint2 code[8], scale[2];
     auto load_ids = [&](int unit) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) id[i] = unit < end ? row_of(w, unit * 32 + r0 + 16 * i) : -1;
     };
-    struct Unit {
-      uint2 code[8], scale[2];
-    };
-    auto load_unit = [&](Unit& c) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint8_t* src = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;
-        c.scale[i] = make_uint2(0u, 0u);
-        if (id[i] >= 0) c.scale[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
-#pragma unroll
-        for (int a = 0; a < 4; ++a) c.code[i * 4 + a] = load_code<kFmt>(src, static_cast<int>(rank) * 256 + a * 64 + piece * 8);
-      }
-    };
-    auto write_unit = [&](int g, const Unit& c) {
-      if (!wait_warp(sb + kVEmpty + 8 * g, parity, p.a.err)) return false;
+    const int entry = static_cast<int>(rank) * 256 + piece * 8;
+    const int begin = w.tile0 * kVUnits;
+    load_ids(begin);
+    // The first turn only asks for the first unit.
+#pragma unroll 1
+    for (int unit = begin - 1; unit < end; ++unit) {
+      const int g = unit & (kVUnits - 1);
+      const bool real = unit >= begin;
+      if (real && !wait_warp(sb + kVEmpty + 8 * g, parity, p.a.err)) return;
       const uint32_t dst = dst0 + g * kVUnitBytes;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* src = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;   // of the next unit
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
-          st_shared16(dst + a * kVAtom + i * 2048,
-                      kv_decode8<kFmt>(c.code[i * 4 + a].x, c.code[i * 4 + a].y,
-                                       kv_scale(__byte_perm(a < 2 ? c.scale[i].x : c.scale[i].y, 0u, sel + 2 * (a & 1)))));
-      unit_ready(sb + kVFull + 8 * g);
-      return true;
-    };
-    Unit even, odd;
-    int unit = w.tile0 * kVUnits;
-    load_ids(unit);
-    load_unit(even);
-    load_ids(unit + 1);
-    load_unit(odd);
-    load_ids(unit + 2);
-#pragma unroll 1
-    for (; unit < end; unit += 2) {
-      const int g = unit & (kVUnits - 1);
-      if (!write_unit(g, even)) return;
-      if (unit + 2 < end) load_unit(even);
-      load_ids(unit + 3);
-      if (!write_unit(g + 1, odd)) return;
-      if (unit + 3 < end) load_unit(odd);
-      load_ids(unit + 4);
-      if (g) parity ^= 1u;
-    }
-  }
-}
-
-// Brings bf16 rows by TMA: one thread asks for those of S and one for those of O,
-// and a warp each passes on what has landed.  Rows behind the prefix are cleared in
-// O's operand: P is 0 there, but 0 times a stale NaN is not.
-__device__ __forceinline__ void ask_keys(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
-  uint32_t parity = 1;
-  for (Items it(p); it.next(p);)
-    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
-      const int row = tile * kTile + static_cast<int>(rank) * 64;
-      for (int u = 0; u < kKUnits; ++u) {
-        if (!wait_one(sb + kKEmpty + 8 * u, parity, p.a.err)) return;
-        const uint32_t bar = sb + kLanded + 8 * u;
-        const int nb = u < 4 ? 2 : 1;
-        bar_expect(bar, nb * kBlockBytes);
-        for (int x = 0; x < nb; ++x)
-          for (int h = 0; h < 2; ++h)   // 32 rows
-            tma_3d(sb + kOffK + (2 * u + x) * kBlockBytes + h * kVAtom, map, bar, (2 * u + x) * 64, row + h * 32, it.w.seq);
-        if (tile + 2 < it.w.tile1)      // the same place two tiles ahead into L2
-          for (int x = 0; x < nb; ++x)
-            for (int h = 0; h < 2; ++h) tma_l2_3d(map, (2 * u + x) * 64, row + 2 * kTile + h * 32, it.w.seq);
+        for (int a = 0; a < 4; ++a) {
+          const uint4 y = kv_decode8<kFmt>(code[i * 4 + a].x, code[i * 4 + a].y,
+                                           kv_scale(__byte_perm(a < 2 ? scale[i].x : scale[i].y, 0u, sel + 2 * (a & 1))));
+          if (real) st_shared16(dst + a * kVAtom + i * 2048, y);
+          code[i * 4 + a] = load_code<kFmt>(src, entry + a * 64);
+        }
+        scale[i] = make_uint2(0u, 0u);
+        if (id[i] >= 0) scale[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
       }
-    }
-}
-__device__ __forceinline__ void ask_values(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
-  uint32_t parity = 1;
-  for (Items it(p); it.next(p);)
-    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u)
-      for (int g = 0; g < kVUnits; ++g) {
-        if (!wait_one(sb + kVEmpty + 8 * g, parity, p.a.err)) return;
-        const uint32_t bar = sb + kLanded + 8 * (kKUnits + g);
-        bar_expect(bar, kVUnitBytes);
-        for (int a = 0; a < 4; ++a)
-          tma_3d(sb + kOffV + g * kVUnitBytes + a * kVAtom, map, bar, static_cast<int>(rank) * 256 + a * 64,
-                 tile * kTile + g * 32, it.w.seq);
-      }
-}
-__device__ __forceinline__ void pass_keys(const MlaParams& p, uint32_t sb) {
-  uint32_t parity = 0;
-  for (Items it(p); it.next(p);)
-    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u)
-      for (int u = 0; u < kKUnits; ++u) {
-        if (!wait_one(sb + kLanded + 8 * u, parity, p.a.err)) return;
-        arrive_in(sb + kKFull + 8 * u, 0);
-      }
-}
-__device__ __forceinline__ void pass_values(const MlaParams& p, int lane, uint32_t sb) {
-  uint32_t parity = 0;
-  for (Items it(p); it.next(p);)
-    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u)
-      for (int g = 0; g < kVUnits; ++g) {
-        if (!wait_warp(sb + kLanded + 8 * (kKUnits + g), parity, p.a.err)) return;
-        const int live = min(max(it.w.n - tile * kTile - g * 32, 0), 32);   // rows of this unit that exist
-        for (int a = 0; a < 4; ++a)
-          for (int c = live * 8 + lane; c < 32 * 8; c += 32)   // whole rows: the swizzle does not matter
-            st_shared16(sb + kOffV + g * kVUnitBytes + a * kVAtom + c * 16, make_uint4(0u, 0u, 0u, 0u));
+      load_ids(unit + 2);
+      if (real) {
         unit_ready(sb + kVFull + 8 * g);
+        if (g == kVUnits - 1) parity ^= 1u;
       }
+    }
+  }
 }
 
-// Brings the queries of this CTA's heads, an item at a time.
-__device__ __forceinline__ void bring_queries(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
-  uint32_t parity = 0;
-  for (Items it(p); it.next(p); parity ^= 1u) {
-    if (!wait_one(sb + kQEmpty, parity ^ 1u, p.a.err)) return;
+// Brings the queries of this CTA's heads and, of a bf16 cache, the rows, by TMA in
+// the order in which the products take them: the rows for S of a tile, then those
+// for O of the tile before.
+template <bool kRows>
+__device__ __forceinline__ void ask(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
+  uint32_t items = 0, tiles = 0;       // so far
+  int last_tile = 0, last_seq = 0;     // the tile before
+  auto values = [&] {
+#pragma unroll 1
+    for (int g = 0; g < kVUnits; ++g) {
+      if (!wait_one(sb + kVEmpty + 8 * g, (tiles & 1), p.a.err)) return false;   // tile number tiles - 1
+      const uint32_t bar = sb + kVLanded + 8 * g;
+      bar_expect(bar, kVUnitBytes);
+#pragma unroll 1
+      for (int a = 0; a < 4; ++a)
+        tma_3d(sb + kOffV + g * kVUnitBytes + a * kVAtom, map, bar, static_cast<int>(rank) * 256 + a * 64,
+               last_tile * kTile + g * 32, last_seq);
+    }
+    return true;
+  };
+  for (Items it(p); it.next(p); ++items) {
+    if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
     bar_expect(sb + kQFull, kBlocks * kBlockBytes);
+#pragma unroll 1
     for (int b = 0; b < kBlocks; ++b)
-      tma_2d(sb + kOffQ + b * kBlockBytes, map, sb + kQFull, b * 64, it.w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
-    if (!wait_one(sb + kQFull, parity, p.a.err)) return;
-    arrive_in(sb + kQReady, 0);
+      tma_2d(sb + kOffQ + b * kBlockBytes, q_map, sb + kQFull, b * 64, it.w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
+    for (int tile = it.w.tile0; kRows && tile < it.w.tile1; ++tile) {
+      const int row = tile * kTile + static_cast<int>(rank) * 64;
+#pragma unroll 1
+      for (int u = 0; u < kKUnits; ++u) {
+        if (!wait_one(sb + kKEmpty + 8 * u, (tiles & 1) ^ 1u, p.a.err)) return;
+        const uint32_t bar = sb + kKLanded + 8 * u;
+        bar_expect(bar, (u < 4 ? 2 : 1) * kBlockBytes);
+#pragma unroll 1
+        for (int x = 0; x < (u < 4 ? 4 : 2); ++x) {   // 32 rows of a block
+          const int b = 2 * u + (x >> 1), y = row + (x & 1) * 32;
+          tma_3d(sb + kOffK + b * kBlockBytes + (x & 1) * kVAtom, map, bar, b * 64, y, it.w.seq);
+          if (tile + 2 < it.w.tile1) tma_l2_3d(map, b * 64, y + 2 * kTile, it.w.seq);   // two tiles ahead into L2
+        }
+      }
+      if (tiles && !values()) return;
+      last_tile = tile;
+      last_seq = it.w.seq;
+      ++tiles;
+    }
   }
+  if (kRows && tiles) values();
+}
+// Passes on to the first CTA what has landed, in the same order.  bf16 rows behind
+// the prefix are cleared in O's operand: P is 0 there, but 0 times a stale NaN is not.
+template <bool kRows>
+__device__ __forceinline__ void pass(const MlaParams& p, int lane, uint32_t sb) {
+  uint32_t items = 0, tiles = 0;
+  int last_live = 0;                   // rows of the tile before that exist
+  auto values = [&] {
+#pragma unroll 1
+    for (int g = 0; g < kVUnits; ++g) {
+      if (!wait_warp(sb + kVLanded + 8 * g, (tiles & 1) ^ 1u, p.a.err)) return false;
+      const int live = min(max(last_live - g * 32, 0), 32);
+#pragma unroll 1
+      for (int a = 0; a < 4; ++a)
+#pragma unroll 1
+        for (int c = live * 8 + lane; c < 32 * 8; c += 32)   // whole rows: the swizzle does not matter
+          st_shared16(sb + kOffV + g * kVUnitBytes + a * kVAtom + c * 16, make_uint4(0u, 0u, 0u, 0u));
+      unit_ready(sb + kVFull + 8 * g);
+    }
+    return true;
+  };
+  for (Items it(p); it.next(p); ++items) {
+    if (!wait_warp(sb + kQFull, items & 1, p.a.err)) return;
+    if (lane == 0) arrive_in(sb + kQReady, 0);
+    for (int tile = it.w.tile0; kRows && tile < it.w.tile1; ++tile) {
+#pragma unroll 1
+      for (int u = 0; u < kKUnits; ++u) {
+        if (!wait_warp(sb + kKLanded + 8 * u, tiles & 1, p.a.err)) return;
+        if (lane == 0) arrive_in(sb + kKFull + 8 * u, 0);
+      }
+      if (tiles && !values()) return;
+      last_live = it.w.n - tile * kTile;
+      ++tiles;
+    }
+  }
+  if (kRows && tiles) values();
 }
 
 // Issues the products of both CTAs, a warp of the first: S of tile n + 1, then
@@ -582,14 +567,21 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
   uint32_t* err = p.a.err;
   const bool leader = elect_one();
   Items si(p), oi(p);
-  bool s_any = si.next(p), o_any = oi.next(p), ok = true;
-  int s_tile = s_any ? si.w.tile0 : 0, o_tile = s_tile;
+  bool s_any = true, ok = true;
+  int s_tile = 0, o_tile = 0, s_end = 0, o_end = 0;
   uint32_t st = 0, ot = 0;              // tiles so far
-  uint32_t s_items = 0, o_items = 0;    // items finished
-  while (ok && o_any) {
+  uint32_t s_items = 0, o_items = 0;    // items begun
+  while (ok) {
     // S, one tile ahead
     while (ok && s_any && st < ot + 2) {
-      if (s_tile == si.w.tile0) ok = wait_warp(sb + kQReady, s_items & 1, err);
+      if (s_tile == s_end) {
+        s_any = si.next(p);
+        if (!s_any) break;
+        s_tile = si.w.tile0;
+        s_end = si.w.tile1;
+        ok = wait_warp(sb + kQReady, s_items & 1, err);
+        ++s_items;
+      }
       const uint32_t place = st & 1;
       ok = ok && wait_warp(sb + kSEmpty + 8 * place, ((st >> 1) & 1) ^ 1u, err);
       const uint32_t d = tmem + kTmemS + place * 64;
@@ -615,16 +607,17 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
       }
       if (leader) commit_pair(sb + kSFull + 8 * place);
       ++st;
-      if (++s_tile == si.w.tile1) {
-        if (leader) commit_pair(sb + kQEmpty);
-        s_any = si.next(p);
-        s_tile = si.w.tile0;
-        ++s_items;
-      }
+      if (++s_tile == s_end && leader) commit_pair(sb + kQEmpty);
     }
     // O
-    const bool first = o_tile == oi.w.tile0;
-    if (first && o_items) ok = ok && wait_warp(sb + kOEmpty, (o_items - 1) & 1, err);
+    const bool first = o_tile == o_end;
+    if (first) {
+      if (!oi.next(p)) break;
+      o_tile = oi.w.tile0;
+      o_end = oi.w.tile1;
+      if (o_items) ok = ok && wait_warp(sb + kOEmpty, (o_items - 1) & 1, err);
+      ++o_items;
+    }
     ok = ok && wait_warp(sb + kPFull, ot & 1, err);
 #pragma unroll 1
     for (uint32_t g = 0; g < kVUnits && ok; ++g) {
@@ -643,11 +636,7 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
     }
     if (leader) commit_pair(sb + kPvDone);
     ++ot;
-    if (++o_tile == oi.w.tile1) {
-      o_any = oi.next(p);
-      o_tile = oi.w.tile0;
-      ++o_items;
-    }
+    ++o_tile;
   }
   if (leader) commit_pair(sb + kDone);
   __syncwarp();
@@ -664,7 +653,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 2 : 8;   // arriving warps of both CTAs
     for (int i = 0; i < kKUnits; ++i) { bar_init(sb + kKFull + 8 * i, kWriters); bar_init(sb + kKEmpty + 8 * i, 1); }
     for (int i = 0; i < kVUnits; ++i) { bar_init(sb + kVFull + 8 * i, kWriters); bar_init(sb + kVEmpty + 8 * i, 1); }
-    for (int i = 0; i < kKUnits + kVUnits; ++i) bar_init(sb + kLanded + 8 * i, 1);
+    for (int i = 0; i < kKUnits + kVUnits; ++i) bar_init(sb + kKLanded + 8 * i, 1);
     for (int i = 0; i < 2; ++i) { bar_init(sb + kSFull + 8 * i, 1); bar_init(sb + kSEmpty + 8 * i, 8); }
     bar_init(sb + kPFull, 8);
     bar_init(sb + kPvDone, 1);
@@ -699,26 +688,16 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       if (rank == 0) multiply(p, tmem, sb);
       wait_all(sb, err);   // nothing reads this CTA's memory any more
       __syncwarp();
-    } else if (warp == kQWarp) {
-      if (elect_one()) bring_queries(p, rank, &q_map, sb);
+    } else if (warp == kMmaWarp + 1) {
+      if (elect_one()) ask<kFmt == MISA_KV_BF16>(p, rank, &q_map, &row_map, sb);
       __syncwarp();
+    } else if (warp == kMmaWarp + 2) {
+      pass<kFmt == MISA_KV_BF16>(p, lane, sb);
     }
   } else if (warp >= kVWarp0) {
-    if constexpr (kFmt == MISA_KV_BF16) {
-      if (warp == kVWarp0 && elect_one()) ask_values(p, rank, &row_map, sb);
-      if (warp == kVWarp0 + 1) pass_values(p, lane, sb);
-      __syncwarp();
-    } else {
-      bring_values<kFmt>(p, rank, tid - kVWarp0 * 32, sb);
-    }
+    if constexpr (kFmt != MISA_KV_BF16) bring_values<kFmt>(p, rank, tid - kVWarp0 * 32, sb);
   } else if (warp >= kKWarp0) {
-    if constexpr (kFmt == MISA_KV_BF16) {
-      if (warp == kKWarp0 && elect_one()) ask_keys(p, rank, &row_map, sb);
-      if (warp == kKWarp0 + 1 && elect_one()) pass_keys(p, sb);
-      __syncwarp();
-    } else {
-      bring_keys<kFmt>(p, rank, tid - kKWarp0 * 32, sb);
-    }
+    if constexpr (kFmt != MISA_KV_BF16) bring_keys<kFmt>(p, rank, tid - kKWarp0 * 32, sb);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ------------------------------------------------------------ softmax and output
@@ -862,24 +841,23 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       const float inv = any ? 1.f / l : 0.f;
       uint8_t* out = reinterpret_cast<uint8_t*>(a.out + (row0 + h0) * kDv + half * 256);
 #pragma unroll 1
-      for (int o = 0; o < 256; o += 64) {
+      for (int o = 0; o < 256; o += 32) {
+        uint32_t v[32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
-          if (have) {
-            tmem_ld32(t_lane + o + q * 32, v);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t x[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              x[u] = have && any ? pack_bf16(__uint_as_float(v[8 * j + 2 * u]) * inv, __uint_as_float(v[8 * j + 2 * u + 1]) * inv) : 0u;
-            st_shared16(turn + lane * 128 + (((q * 4 + j) ^ (lane & 7)) << 4), make_uint4(x[0], x[1], x[2], x[3]));
-          }
+        for (int j = 0; j < 32; ++j) v[j] = 0u;
+        if (have) {
+          tmem_ld32(t_lane + o, v);
+          tmem_wait_ld();
         }
-        turned(out + o * 2, kDv * 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            x[u] = pack_bf16(__uint_as_float(v[8 * j + 2 * u]) * inv, __uint_as_float(v[8 * j + 2 * u + 1]) * inv);
+          st_shared16(turn + lane * 128 + ((((o >> 3) & 4) + j) ^ (lane & 7)) * 16, make_uint4(x[0], x[1], x[2], x[3]));
+        }
+        if (o & 32) turned(out + (o - 32) * 2, kDv * 2);
       }
     }
     if (ntiles > 0 && ok) {   // O has been read
