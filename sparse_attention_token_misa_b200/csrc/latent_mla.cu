@@ -39,14 +39,14 @@
 // around 3 us a tile.)  Few queries: the rows of each are split over several
 // items, whose partial sums a second kernel joins in a fixed order.
 //
-// Roles (512 threads a CTA, by warpgroups): warps 0-3 softmax and output (a lane of
-// TMEM each), warps 4-7 bring quantised rows for S, warps 8-11 for O, warp 12 has
-// TMEM and, in the first CTA, issues the MMAs, warp 13 asks for what comes by TMA and
-// warp 14 passes on what has landed.  The softmax
-// holds a tile's 64 scores a lane and more, so the last warpgroup gives it 48 of its
-// registers a thread.  Shared memory is addressed from one 32-bit base: with a
-// pointer a barrier the kernel spilled, and what shared memory leaves of L1 does
-// not hold the stack.  Waits are bounded.
+// Roles, by warpgroups: warps 0-3 softmax and output (a lane of TMEM each); 8 warps
+// that bring quantised rows for S and 8 for O (none of either for bf16 rows); then
+// one warp that has TMEM and, in the first CTA, issues the MMAs, one that asks for
+// what comes by TMA and one that passes on what has landed.  The softmax holds a
+// tile's 64 scores a lane and more, so the other warpgroups of the large block give
+// it registers.  Shared memory is addressed from one 32-bit base: with a pointer a
+// barrier the kernel spilled, and what shared memory leaves of L1 does not hold the
+// stack.  Waits are bounded.
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"
@@ -89,7 +89,10 @@ constexpr uint32_t kOffTmem = kDone + 8;
 constexpr uint32_t kOffRed = (kOffTmem + 8 + 15) / 16 * 16;   // [3][128] floats
 constexpr int kSmemBytes = kOffRed + 3 * 128 * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-constexpr int kKWarp0 = 4, kVWarp0 = 8, kMmaWarp = 12, kThreads = 16 * 32;
+// Warps: 0-3 softmax and output, then those that bring quantised rows, then four more.
+constexpr int kKWarps = 8, kVWarps = 8;
+constexpr int first_other_warp(int fmt) { return fmt == MISA_KV_BF16 ? 4 : 4 + kKWarps + kVWarps; }
+constexpr int block_threads(int fmt) { return (first_other_warp(fmt) + 4) * 32; }
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 64 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -341,31 +344,31 @@ __device__ __forceinline__ void unit_ready(uint32_t full) {
   if ((threadIdx.x & 31) == 0) arrive_in(full, 0);
 }
 
-// Brings quantised rows for S, 128 threads: thread = (rows r0 + 16 i, piece of 8
-// entries) of each block.  An absent row is any row's codes with a scale of zero.
+// Brings quantised rows for S, 256 threads: thread = (rows r0 and r0 + 32, piece of
+// 8 entries) of each block.  An absent row is any row's codes with a scale of zero.
 // Where a piece has been widened, the same piece of the next unit is asked for into
 // its registers.
 template <int kFmt>
 __device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7;
-  const uint32_t dst0 = sb + kOffK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 16 apart: the same swizzle
+  const uint32_t dst0 = sb + kOffK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 32 apart: the same swizzle
   const int own = static_cast<int>(rank) * 64;
   const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
   uint32_t* err = p.a.err;
   uint32_t parity = 1;
   for (Items it(p); it.next(p);) {
     const Work& w = it.w;
-    int32_t id[4];
-    const uint8_t* src[4];
-    bool here[4];
-    uint2 code[8];
-    uint32_t scale[4];
-    uint4 rope[4];
+    int32_t id[2];
+    const uint8_t* src[2];
+    bool here[2];
+    uint2 code[4];
+    uint32_t scale[2];
+    uint4 rope[2];
     auto load_ids = [&](int tile) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int s = tile * kTile + own + r0 + 16 * i;
+      for (int i = 0; i < 2; ++i) {
+        const int s = tile * kTile + own + r0 + 32 * i;
         id[i] = tile < w.tile1 && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
       }
     };
@@ -377,30 +380,30 @@ __device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, in
       const bool real = unit >= 4 * w.tile0;
       if (u == 3) {   // on to the rows of the next tile
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           if (piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(err, MISA_DEVERR_BAD_INDEX);
           here[i] = id[i] >= 0 && id[i] < w.L;
           src[i] = w.base + static_cast<int64_t>(here[i] ? id[i] : 0) * kRow;
         }
         load_ids(tile + 2);
-        // those two tiles ahead into L2: lines of 128 bytes, two threads a row
-        const int far = (tile + 3) * kTile + own + (tid >> 1);
+        // those two tiles ahead into L2: lines of 128 bytes, four threads a row
+        const int far = (tile + 3) * kTile + own + (tid >> 2);
         if (tile + 3 < w.tile1 && far < w.n) {
           const int32_t fid = row_of(w, far);
-          const uint8_t* row = w.base + static_cast<int64_t>(max(fid, 0)) * kRow + (tid & 1) * 128;
+          const uint8_t* row = w.base + static_cast<int64_t>(max(fid, 0)) * kRow + (tid & 3) * 128;
 #pragma unroll
-          for (int o = 0; o < kRow; o += 256)
-            if (o + (tid & 1) * 128 < kRow) l2_prefetch(row + o);
+          for (int o = 0; o < kRow; o += 512)
+            if (o + (tid & 3) * 128 < kRow) l2_prefetch(row + o);
         }
       }
       if (real && !wait_warp(sb + kKEmpty + 8 * u, parity, err)) return;
       const uint32_t dst = dst0 + u * 2 * kBlockBytes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint4 y = kv_decode8<kFmt>(code[2 * i + x].x, code[2 * i + x].y, kv_scale(__byte_perm(scale[i], 0u, sel + 2 * x)));
-          if (real) st_shared16(dst + x * kBlockBytes + i * 2048, y);
+          if (real) st_shared16(dst + x * kBlockBytes + i * 4096, y);
           code[2 * i + x] = load_code<kFmt>(src[i], next * 128 + x * 64 + piece * 8);
         }
         scale[i] = 0u;
@@ -411,12 +414,12 @@ __device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, in
         if (real) {
           if (!wait_warp(sb + kKEmpty + 8 * 4, parity, err)) return;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 2048, rope[i]);
+          for (int i = 0; i < 2; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 4096, rope[i]);
           unit_ready(sb + kKFull + 8 * 4);
           parity ^= 1u;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           rope[i] = make_uint4(0u, 0u, 0u, 0u);
           if (here[i]) rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
         }
@@ -425,7 +428,7 @@ __device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, in
   }
 }
 
-// Brings quantised rows for O, 128 threads: entries [256 rank, 256 rank + 256) of 32
+// Brings quantised rows for O, 256 threads (a row r0 each): entries [256 rank, 256 rank + 256) of 32
 // rows a unit.
 template <int kFmt>
 __device__ __forceinline__ void bring_values(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
@@ -437,11 +440,10 @@ __device__ __forceinline__ void bring_values(const MlaParams& p, uint32_t rank, 
   for (Items it(p); it.next(p);) {
     const Work& w = it.w;
     const int end = w.tile1 * kVUnits;   // units are counted over the tiles
-    int32_t id[2];
-    uint2 code[8], scale[2];
+    int32_t id;
+    uint2 code[4], scale;
     auto load_ids = [&](int unit) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) id[i] = unit < end ? row_of(w, unit * 32 + r0 + 16 * i) : -1;
+      id = unit < end ? row_of(w, unit * 32 + r0) : -1;
     };
     const int entry = static_cast<int>(rank) * 256 + piece * 8;
     const int begin = w.tile0 * kVUnits;
@@ -453,19 +455,15 @@ __device__ __forceinline__ void bring_values(const MlaParams& p, uint32_t rank, 
       const bool real = unit >= begin;
       if (real && !wait_warp(sb + kVEmpty + 8 * g, parity, p.a.err)) return;
       const uint32_t dst = dst0 + g * kVUnitBytes;
+      const uint8_t* src = w.base + static_cast<int64_t>(max(id, 0)) * kRow;   // of the next unit
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint8_t* src = w.base + static_cast<int64_t>(max(id[i], 0)) * kRow;   // of the next unit
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const uint4 y = kv_decode8<kFmt>(code[i * 4 + a].x, code[i * 4 + a].y,
-                                           kv_scale(__byte_perm(a < 2 ? scale[i].x : scale[i].y, 0u, sel + 2 * (a & 1))));
-          if (real) st_shared16(dst + a * kVAtom + i * 2048, y);
-          code[i * 4 + a] = load_code<kFmt>(src, entry + a * 64);
-        }
-        scale[i] = make_uint2(0u, 0u);
-        if (id[i] >= 0) scale[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
+      for (int a = 0; a < 4; ++a) {
+        const uint4 y = kv_decode8<kFmt>(code[a].x, code[a].y, kv_scale(__byte_perm(a < 2 ? scale.x : scale.y, 0u, sel + 2 * (a & 1))));
+        if (real) st_shared16(dst + a * kVAtom, y);
+        code[a] = load_code<kFmt>(src, entry + a * 64);
       }
+      scale = make_uint2(0u, 0u);
+      if (id >= 0) scale = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
       load_ids(unit + 2);
       if (real) {
         unit_ready(sb + kVFull + 8 * g);
@@ -643,16 +641,18 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(block_threads(kFmt), 1) __cluster_dims__(2, 1, 1)
 latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap row_map, const MlaParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  constexpr int kMmaWarp = first_other_warp(kFmt);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   if (tid == 0) {
-    constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 2 : 8;   // arriving warps of both CTAs
-    for (int i = 0; i < kKUnits; ++i) { bar_init(sb + kKFull + 8 * i, kWriters); bar_init(sb + kKEmpty + 8 * i, 1); }
-    for (int i = 0; i < kVUnits; ++i) { bar_init(sb + kVFull + 8 * i, kWriters); bar_init(sb + kVEmpty + 8 * i, 1); }
+    constexpr uint32_t kKWriters = kFmt == MISA_KV_BF16 ? 2 : 2 * kKWarps;   // arriving warps of both CTAs
+    constexpr uint32_t kVWriters = kFmt == MISA_KV_BF16 ? 2 : 2 * kVWarps;
+    for (int i = 0; i < kKUnits; ++i) { bar_init(sb + kKFull + 8 * i, kKWriters); bar_init(sb + kKEmpty + 8 * i, 1); }
+    for (int i = 0; i < kVUnits; ++i) { bar_init(sb + kVFull + 8 * i, kVWriters); bar_init(sb + kVEmpty + 8 * i, 1); }
     for (int i = 0; i < kKUnits + kVUnits; ++i) bar_init(sb + kKLanded + 8 * i, 1);
     for (int i = 0; i < 2; ++i) { bar_init(sb + kSFull + 8 * i, 1); bar_init(sb + kSEmpty + 8 * i, 8); }
     bar_init(sb + kPFull, 8);
@@ -682,8 +682,9 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 
   const LatentArgs& a = p.a;
   uint32_t* err = a.err;
+  // (768 threads of 80 registers: 152 + 4 * 64 + 72 of 480 for the six warpgroups)
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (kFmt != MISA_KV_BF16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kMmaWarp) {
       if (rank == 0) multiply(p, tmem, sb);
       wait_all(sb, err);   // nothing reads this CTA's memory any more
@@ -694,12 +695,14 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     } else if (warp == kMmaWarp + 2) {
       pass<kFmt == MISA_KV_BF16>(p, lane, sb);
     }
-  } else if (warp >= kVWarp0) {
-    if constexpr (kFmt != MISA_KV_BF16) bring_values<kFmt>(p, rank, tid - kVWarp0 * 32, sb);
-  } else if (warp >= kKWarp0) {
-    if constexpr (kFmt != MISA_KV_BF16) bring_keys<kFmt>(p, rank, tid - kKWarp0 * 32, sb);
+  } else if (warp >= 4) {
+    if constexpr (kFmt != MISA_KV_BF16) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      if (warp < 4 + kKWarps) bring_keys<kFmt>(p, rank, tid - 128, sb);
+      else bring_values<kFmt>(p, rank, tid - 128 - kKWarps * 32, sb);
+    }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if (kFmt != MISA_KV_BF16) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     // ------------------------------------------------------------ softmax and output
     const int half = warp >> 1;                     // rows [64 half, 64 half + 64) of a tile, entries 256 half .. of O
     const int hl = (warp & 1) * 32 + lane;          // head of this CTA
@@ -967,7 +970,7 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   p.items = a.T * p.nsplit;
   p.by_nsplit = p.nsplit > 1 ? static_cast<uint32_t>(((1ull << 32) + p.nsplit - 1) / p.nsplit) : 0u;
   const int clusters = p.items < kSlots ? p.items : kSlots;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(block_threads(a.fmt)), kSmemBytes, stream, 0, qmap, rmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * a.Hq), dim3(128), 0, stream, 0,
                     static_cast<const float*>(p.part_o), static_cast<const float*>(p.part_ml), a.Hq, p.nsplit, a.out, a.lse);
