@@ -60,23 +60,22 @@ constexpr int kTile = 128;                        // rows of a tile
 constexpr int kHeads = 64;                        // heads of a CTA
 constexpr int kBlocks = kDqk / 64;                // 9
 constexpr uint32_t kBlockBytes = 64 * 128;        // 64 rows (heads) x 64 bf16
-constexpr int kKUnits = 5;                        // S operand: four pairs of blocks, then the rotary block
-constexpr int kVUnits = 4;                        // O operand: 32 rows x 256 entries each
-constexpr uint32_t kVAtom = 32 * 128;             // 32 rows x 64 entries
-constexpr uint32_t kVUnitBytes = 4 * kVAtom;
+constexpr int kUnits = 2;                         // both operands are brought and freed by halves:
+constexpr uint32_t kKUnitBytes = 4 * kBlockBytes; // S: blocks 0..3 and 4..8 of the CTA's 64 rows
+constexpr uint32_t kVUnitBytes = 4 * kBlockBytes; // O: 256 entries of rows 0..63 and 64..127
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + kBlocks * kBlockBytes;
 constexpr uint32_t kOffV = kOffK + kBlocks * kBlockBytes;
-constexpr uint32_t kOffP = kOffV + kVUnits * kVUnitBytes;
+constexpr uint32_t kOffP = kOffV + kUnits * kVUnitBytes;
 constexpr uint32_t kOffBar = kOffP + 2 * kBlockBytes;
 // barriers (of the first CTA where it says so)
-constexpr uint32_t kKFull = kOffBar;              // [5] first CTA: unit brought by both
-constexpr uint32_t kKEmpty = kKFull + 8 * kKUnits;   // [5] multiplied
-constexpr uint32_t kVFull = kKEmpty + 8 * kKUnits;   // [4] first CTA
-constexpr uint32_t kVEmpty = kVFull + 8 * kVUnits;   // [4]
-constexpr uint32_t kKLanded = kVEmpty + 8 * kVUnits;  // [5] bf16: TMA done
-constexpr uint32_t kVLanded = kKLanded + 8 * kKUnits; // [4]
-constexpr uint32_t kSFull = kVLanded + 8 * kVUnits;   // [2] S complete
+constexpr uint32_t kKFull = kOffBar;              // [2] first CTA: unit brought by both
+constexpr uint32_t kVFull = kKFull + 16;          // [2] first CTA
+constexpr uint32_t kKEmpty = kVFull + 16;         // [2] multiplied
+constexpr uint32_t kVEmpty = kKEmpty + 16;        // [2]
+constexpr uint32_t kKLanded = kVEmpty + 16;       // [2] bf16: TMA done
+constexpr uint32_t kVLanded = kKLanded + 16;      // [2]
+constexpr uint32_t kSFull = kVLanded + 16;   // [2] S complete
 constexpr uint32_t kSEmpty = kSFull + 16;         // [2] first CTA: S read by both
 constexpr uint32_t kPFull = kSEmpty + 16;         // first CTA: P written (and O scaled) by both
 constexpr uint32_t kPvDone = kPFull + 8;          // O += P V complete
@@ -90,9 +89,9 @@ constexpr uint32_t kOffRed = (kOffTmem + 8 + 15) / 16 * 16;   // [3][128] floats
 constexpr int kSmemBytes = kOffRed + 3 * 128 * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Warps: 0-3 softmax and output, then those that bring quantised rows, then four more.
-constexpr int kKWarps = 8, kVWarps = 8;
-constexpr int first_other_warp(int fmt) { return fmt == MISA_KV_BF16 ? 4 : 4 + kKWarps + kVWarps; }
-constexpr int block_threads(int fmt) { return (first_other_warp(fmt) + 4) * 32; }
+constexpr int kRowWarps = 8;   // for S, and as many for O
+constexpr int first_other_warp(int fmt) { return fmt == MISA_KV_BF16 ? 4 : 4 + 2 * kRowWarps; }
+constexpr int block_threads(int fmt) { return (first_other_warp(fmt) + (fmt == MISA_KV_BF16 ? 5 : 4)) * 32; }
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 64 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -115,7 +114,16 @@ __device__ __forceinline__ void arrive_in(uint32_t bar, uint32_t rank) {
       "r"(rank)
       : "memory");
 }
-// Whether the phase of `parity` is over.
+// Whether the phase of `parity` is over (try: may sleep a while first).
+__device__ __forceinline__ uint32_t test_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
 __device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -249,7 +257,6 @@ __device__ __forceinline__ void tma_l2_3d(const void* map, int x, int y, int z) 
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
                : "memory");
 }
-__device__ __forceinline__ void l2_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---------------------------------------------------------------- items
 struct MlaParams {
@@ -344,297 +351,277 @@ __device__ __forceinline__ void unit_ready(uint32_t full) {
   if ((threadIdx.x & 31) == 0) arrive_in(full, 0);
 }
 
-// Brings quantised rows for S, 256 threads: thread = (rows r0 and r0 + 32, piece of
-// 8 entries) of each block.  An absent row is any row's codes with a scale of zero.
-// Where a piece has been widened, the same piece of the next unit is asked for into
-// its registers.
+// Brings quantised rows, 256 threads for S and 256 for O (the same code, for the
+// instruction caches' sake): thread = (rows r0 and r0 + 32, piece of 8 entries) of
+// each of a unit's four blocks.  An absent row is any row's codes with scales of
+// zero.  Where a piece has been widened, the same piece of the next unit is asked
+// for into its registers.
 template <int kFmt>
-__device__ __forceinline__ void bring_keys(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
+__device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, bool keys, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7;
-  const uint32_t dst0 = sb + kOffK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 32 apart: the same swizzle
-  const int own = static_cast<int>(rank) * 64;
+  const uint32_t dst0 = sb + (keys ? kOffK : kOffV) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 32 apart: the same swizzle
+  const uint32_t full = sb + (keys ? kKFull : kVFull), empty = sb + (keys ? kKEmpty : kVEmpty);
   const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
-  uint32_t* err = p.a.err;
   uint32_t parity = 1;
   for (Items it(p); it.next(p);) {
     const Work& w = it.w;
+    const int begin = w.tile0 * kUnits, end = w.tile1 * kUnits;   // units are counted over the tiles
     int32_t id[2];
-    const uint8_t* src[2];
-    bool here[2];
-    uint2 code[4];
-    uint32_t scale[2];
-    uint4 rope[2];
-    auto load_ids = [&](int tile) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int s = tile * kTile + own + r0 + 32 * i;
-        id[i] = tile < w.tile1 && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
-      }
-    };
-    load_ids(w.tile0);
-    // Units of the tiles, four pairs each; the first turn only asks for unit 0.
-#pragma unroll 1
-    for (int unit = 4 * w.tile0 - 1; unit < 4 * w.tile1; ++unit) {
-      const int tile = unit >> 2, u = unit & 3, next = (u + 1) & 3;
-      const bool real = unit >= 4 * w.tile0;
-      if (u == 3) {   // on to the rows of the next tile
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(err, MISA_DEVERR_BAD_INDEX);
-          here[i] = id[i] >= 0 && id[i] < w.L;
-          src[i] = w.base + static_cast<int64_t>(here[i] ? id[i] : 0) * kRow;
-        }
-        load_ids(tile + 2);
-        // those two tiles ahead into L2: lines of 128 bytes, four threads a row
-        const int far = (tile + 3) * kTile + own + (tid >> 2);
-        if (tile + 3 < w.tile1 && far < w.n) {
-          const int32_t fid = row_of(w, far);
-          const uint8_t* row = w.base + static_cast<int64_t>(max(fid, 0)) * kRow + (tid & 3) * 128;
-#pragma unroll
-          for (int o = 0; o < kRow; o += 512)
-            if (o + (tid & 3) * 128 < kRow) l2_prefetch(row + o);
-        }
-      }
-      if (real && !wait_warp(sb + kKEmpty + 8 * u, parity, err)) return;
-      const uint32_t dst = dst0 + u * 2 * kBlockBytes;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint4 y = kv_decode8<kFmt>(code[2 * i + x].x, code[2 * i + x].y, kv_scale(__byte_perm(scale[i], 0u, sel + 2 * x)));
-          if (real) st_shared16(dst + x * kBlockBytes + i * 4096, y);
-          code[2 * i + x] = load_code<kFmt>(src[i], next * 128 + x * 64 + piece * 8);
-        }
-        scale[i] = 0u;
-        if (here[i]) scale[i] = __ldg(reinterpret_cast<const uint32_t*>(src[i] + kv_code_bytes(kFmt) + 4 * next));
-      }
-      if (real) unit_ready(sb + kKFull + 8 * u);
-      if (u == 3) {   // the rotary block of this tile, and the next one's asked for
-        if (real) {
-          if (!wait_warp(sb + kKEmpty + 8 * 4, parity, err)) return;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) st_shared16(dst0 + 8 * kBlockBytes + i * 4096, rope[i]);
-          unit_ready(sb + kKFull + 8 * 4);
-          parity ^= 1u;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          rope[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (here[i]) rope[i] = __ldg(reinterpret_cast<const uint4*>(src[i] + kv_rope_offset(kFmt) + piece * 16));
-        }
-      }
-    }
-  }
-}
-
-// Brings quantised rows for O, 256 threads (a row r0 each): entries [256 rank, 256 rank + 256) of 32
-// rows a unit.
-template <int kFmt>
-__device__ __forceinline__ void bring_values(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
-  constexpr int kRow = kv_row_bytes(kFmt);
-  const int r0 = tid >> 3, piece = tid & 7;
-  const uint32_t dst0 = sb + kOffV + r0 * 128 + ((piece ^ (r0 & 7)) << 4);
-  const uint32_t sel = 0x4440u | (piece >> 2);
-  uint32_t parity = 1;
-  for (Items it(p); it.next(p);) {
-    const Work& w = it.w;
-    const int end = w.tile1 * kVUnits;   // units are counted over the tiles
-    int32_t id;
-    uint2 code[4], scale;
     auto load_ids = [&](int unit) {
-      id = unit < end ? row_of(w, unit * 32 + r0) : -1;
+      const int first = keys ? (unit >> 1) * kTile + static_cast<int>(rank) * 64 : unit * 64;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int s = first + r0 + 32 * i;
+        id[i] = unit < end && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
+      }
     };
-    const int entry = static_cast<int>(rank) * 256 + piece * 8;
-    const int begin = w.tile0 * kVUnits;
+    uint2 code[8], scale[2];
+    uint4 rope[2];
     load_ids(begin);
     // The first turn only asks for the first unit.
 #pragma unroll 1
     for (int unit = begin - 1; unit < end; ++unit) {
-      const int g = unit & (kVUnits - 1);
+      const uint32_t u = unit & 1, next = u ^ 1u;
       const bool real = unit >= begin;
-      if (real && !wait_warp(sb + kVEmpty + 8 * g, parity, p.a.err)) return;
-      const uint32_t dst = dst0 + g * kVUnitBytes;
-      const uint8_t* src = w.base + static_cast<int64_t>(max(id, 0)) * kRow;   // of the next unit
+      if (real && !wait_warp(empty + 8 * u, parity, p.a.err)) return;
+      const uint32_t dst = dst0 + u * kKUnitBytes;
+      const int entry = (keys ? static_cast<int>(next) : static_cast<int>(rank)) * 256;   // of the next unit
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const uint4 y = kv_decode8<kFmt>(code[a].x, code[a].y, kv_scale(__byte_perm(a < 2 ? scale.x : scale.y, 0u, sel + 2 * (a & 1))));
-        if (real) st_shared16(dst + a * kVAtom, y);
-        code[a] = load_code<kFmt>(src, entry + a * 64);
+      for (int i = 0; i < 2; ++i) {
+        if (keys && piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(p.a.err, MISA_DEVERR_BAD_INDEX);
+        const bool here = id[i] >= 0 && id[i] < w.L;
+        const uint8_t* src = w.base + static_cast<int64_t>(here ? id[i] : 0) * kRow;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint4 y = kv_decode8<kFmt>(code[i * 4 + b].x, code[i * 4 + b].y,
+                                           kv_scale(__byte_perm(b < 2 ? scale[i].x : scale[i].y, 0u, sel + 2 * (b & 1))));
+          if (real) st_shared16(dst + b * kBlockBytes + i * 4096, y);
+          code[i * 4 + b] = load_code<kFmt>(src, entry + b * 64 + piece * 8);
+        }
+        scale[i] = make_uint2(0u, 0u);
+        if (here) scale[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + (entry >> 5)));
+        if (keys && u) {   // the rotary block, and the next tile's asked for
+          if (real) st_shared16(dst + 4 * kBlockBytes + i * 4096, rope[i]);
+          rope[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (here) rope[i] = __ldg(reinterpret_cast<const uint4*>(src + kv_rope_offset(kFmt) + piece * 16));
+        }
       }
-      scale = make_uint2(0u, 0u);
-      if (id >= 0) scale = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + rank * 8));
       load_ids(unit + 2);
       if (real) {
-        unit_ready(sb + kVFull + 8 * g);
-        if (g == kVUnits - 1) parity ^= 1u;
+        unit_ready(full + 8 * u);
+        parity ^= u;
       }
     }
   }
 }
 
-// Brings the queries of this CTA's heads and, of a bf16 cache, the rows, by TMA in
-// the order in which the products take them: the rows for S of a tile, then those
-// for O of the tile before.
-template <bool kRows>
-__device__ __forceinline__ void ask(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
-  uint32_t items = 0, tiles = 0;       // so far
-  int last_tile = 0, last_seq = 0;     // the tile before
-  auto values = [&] {
+// Asks the quantised rows of the tile after the next into L2, a warp: in a prefix one
+// request for the CTA's 64 rows, else line by line.
+template <int kFmt>
+__device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, int lane, uint32_t sb) {
+  constexpr int kRow = kv_row_bytes(kFmt);
+  uint32_t parity = 1;
+  for (Items it(p); it.next(p);) {
+    const Work& w = it.w;
+    for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u) {
+      // Goes on with the tiles: S of this one waits for the arrival, so that no phase
+      // can pass by unseen.
+      if (!wait_warp(sb + kKEmpty + 8, parity, p.a.err)) return;
+      if (lane == 0) arrive_in(sb + kKFull + 8, 0);
+      const int first = (tile + 2) * kTile + static_cast<int>(rank) * 64;
+      if (tile + 2 >= w.tile1) continue;
+      if (!w.idx) {
+        const int rows = min(64, w.n - first);
+        if (lane == 0 && rows > 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w.base + static_cast<int64_t>(first) * kRow), "r"(rows * kRow)
+                       : "memory");
+        continue;
+      }
 #pragma unroll 1
-    for (int g = 0; g < kVUnits; ++g) {
-      if (!wait_one(sb + kVEmpty + 8 * g, (tiles & 1), p.a.err)) return false;   // tile number tiles - 1
-      const uint32_t bar = sb + kVLanded + 8 * g;
-      bar_expect(bar, kVUnitBytes);
+      for (int r = lane; r < 64; r += 32) {
+        const int32_t id = row_of(w, first + r);
+        if (id < 0) continue;
+        const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow;
 #pragma unroll 1
-      for (int a = 0; a < 4; ++a)
-        tma_3d(sb + kOffV + g * kVUnitBytes + a * kVAtom, map, bar, static_cast<int>(rank) * 256 + a * 64,
-               last_tile * kTile + g * 32, last_seq);
+        for (int o = 0; o < kRow; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + o));
+      }
     }
-    return true;
-  };
+  }
+}
+
+// Brings the queries of this CTA's heads and, of a bf16 cache, the rows for S, by
+// TMA; one thread.
+template <bool kRows>
+__device__ __forceinline__ void ask_keys(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
+  uint32_t items = 0, parity = 1;
   for (Items it(p); it.next(p); ++items) {
     if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
     bar_expect(sb + kQFull, kBlocks * kBlockBytes);
 #pragma unroll 1
     for (int b = 0; b < kBlocks; ++b)
       tma_2d(sb + kOffQ + b * kBlockBytes, q_map, sb + kQFull, b * 64, it.w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
-    for (int tile = it.w.tile0; kRows && tile < it.w.tile1; ++tile) {
+    for (int tile = it.w.tile0; kRows && tile < it.w.tile1; ++tile, parity ^= 1u) {
       const int row = tile * kTile + static_cast<int>(rank) * 64;
 #pragma unroll 1
-      for (int u = 0; u < kKUnits; ++u) {
-        if (!wait_one(sb + kKEmpty + 8 * u, (tiles & 1) ^ 1u, p.a.err)) return;
-        const uint32_t bar = sb + kKLanded + 8 * u;
-        bar_expect(bar, (u < 4 ? 2 : 1) * kBlockBytes);
-#pragma unroll 1
-        for (int x = 0; x < (u < 4 ? 4 : 2); ++x) {   // 32 rows of a block
-          const int b = 2 * u + (x >> 1), y = row + (x & 1) * 32;
-          tma_3d(sb + kOffK + b * kBlockBytes + (x & 1) * kVAtom, map, bar, b * 64, y, it.w.seq);
-          if (tile + 2 < it.w.tile1) tma_l2_3d(map, b * 64, y + 2 * kTile, it.w.seq);   // two tiles ahead into L2
+      for (int b = 0; b < kBlocks; ++b) {
+        const uint32_t u = b >= 4;
+        if ((b & 3) == 0 && b < 8) {
+          if (!wait_one(sb + kKEmpty + 8 * u, parity, p.a.err)) return;
+          bar_expect(sb + kKLanded + 8 * u, (u ? 5 : 4) * kBlockBytes);
         }
+        tma_3d(sb + kOffK + b * kBlockBytes, map, sb + kKLanded + 8 * u, b * 64, row, it.w.seq);
+        if (tile + 2 < it.w.tile1) tma_l2_3d(map, b * 64, row + 2 * kTile, it.w.seq);   // two tiles ahead into L2
       }
-      if (tiles && !values()) return;
-      last_tile = tile;
-      last_seq = it.w.seq;
-      ++tiles;
     }
   }
-  if (kRows && tiles) values();
 }
-// Passes on to the first CTA what has landed, in the same order.  bf16 rows behind
-// the prefix are cleared in O's operand: P is 0 there, but 0 times a stale NaN is not.
-template <bool kRows>
-__device__ __forceinline__ void pass(const MlaParams& p, int lane, uint32_t sb) {
-  uint32_t items = 0, tiles = 0;
-  int last_live = 0;                   // rows of the tile before that exist
-  auto values = [&] {
+// The same for O's rows.
+__device__ __forceinline__ void ask_values(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
+  uint32_t parity = 1;
+  for (Items it(p); it.next(p);)
 #pragma unroll 1
-    for (int g = 0; g < kVUnits; ++g) {
-      if (!wait_warp(sb + kVLanded + 8 * g, (tiles & 1) ^ 1u, p.a.err)) return false;
-      const int live = min(max(last_live - g * 32, 0), 32);
+    for (int unit = it.w.tile0 * kUnits; unit < it.w.tile1 * kUnits; ++unit) {
+      const uint32_t g = unit & 1;
+      if (!wait_one(sb + kVEmpty + 8 * g, parity, p.a.err)) return;
+      bar_expect(sb + kVLanded + 8 * g, kVUnitBytes);
 #pragma unroll 1
       for (int a = 0; a < 4; ++a)
-#pragma unroll 1
-        for (int c = live * 8 + lane; c < 32 * 8; c += 32)   // whole rows: the swizzle does not matter
-          st_shared16(sb + kOffV + g * kVUnitBytes + a * kVAtom + c * 16, make_uint4(0u, 0u, 0u, 0u));
-      unit_ready(sb + kVFull + 8 * g);
+        tma_3d(sb + kOffV + g * kVUnitBytes + a * kBlockBytes, map, sb + kVLanded + 8 * g, static_cast<int>(rank) * 256 + a * 64,
+               unit * 64, it.w.seq);
+      parity ^= g;
     }
-    return true;
-  };
+}
+// Pass on to the first CTA what has landed, a warp each.
+template <bool kRows>
+__device__ __forceinline__ void pass_keys(const MlaParams& p, int lane, uint32_t sb) {
+  uint32_t items = 0, parity = 0;
   for (Items it(p); it.next(p); ++items) {
     if (!wait_warp(sb + kQFull, items & 1, p.a.err)) return;
     if (lane == 0) arrive_in(sb + kQReady, 0);
-    for (int tile = it.w.tile0; kRows && tile < it.w.tile1; ++tile) {
 #pragma unroll 1
-      for (int u = 0; u < kKUnits; ++u) {
-        if (!wait_warp(sb + kKLanded + 8 * u, tiles & 1, p.a.err)) return;
-        if (lane == 0) arrive_in(sb + kKFull + 8 * u, 0);
-      }
-      if (tiles && !values()) return;
-      last_live = it.w.n - tile * kTile;
-      ++tiles;
+    for (int unit = it.w.tile0 * kUnits; kRows && unit < it.w.tile1 * kUnits; ++unit) {
+      const uint32_t u = unit & 1;
+      if (!wait_warp(sb + kKLanded + 8 * u, parity, p.a.err)) return;
+      if (lane == 0) arrive_in(sb + kKFull + 8 * u, 0);
+      parity ^= u;
     }
   }
-  if (kRows && tiles) values();
+}
+// Rows behind the prefix are cleared: P is 0 there, but 0 times a stale NaN is not.
+__device__ __forceinline__ void pass_values(const MlaParams& p, int lane, uint32_t sb) {
+  uint32_t parity = 0;
+  for (Items it(p); it.next(p);)
+#pragma unroll 1
+    for (int unit = it.w.tile0 * kUnits; unit < it.w.tile1 * kUnits; ++unit) {
+      const uint32_t g = unit & 1;
+      if (!wait_warp(sb + kVLanded + 8 * g, parity, p.a.err)) return;
+      const int live = min(max(it.w.n - unit * 64, 0), 64);
+#pragma unroll 1
+      for (int a = 0; a < 4; ++a)
+#pragma unroll 1
+        for (int c = live * 8 + lane; c < 64 * 8; c += 32)   // whole rows: the swizzle does not matter
+          st_shared16(sb + kOffV + g * kVUnitBytes + a * kBlockBytes + c * 16, make_uint4(0u, 0u, 0u, 0u));
+      unit_ready(sb + kVFull + 8 * g);
+      parity ^= g;
+    }
 }
 
-// Issues the products of both CTAs, a warp of the first: S of tile n + 1, then
-// O += P V of tile n, over the items.  The warp waits as a whole and one lane issues
-// what a unit allows.
+// Issues the products of both CTAs, a warp of the first.  Two rows of work over the
+// items, S of one tile after the other and O += P V; whatever has its operands next
+// is issued, O first.  The warp looks at all the barriers together, and one lane
+// issues a unit.
 __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint32_t sb) {
-  uint32_t* err = p.a.err;
   const bool leader = elect_one();
   Items si(p), oi(p);
-  bool s_any = true, ok = true;
-  int s_tile = 0, o_tile = 0, s_end = 0, o_end = 0;
+  int s_left = 0, o_left = 0;           // tiles of the item at hand
+  bool s_any = true, s_first = false, o_first = false;
   uint32_t st = 0, ot = 0;              // tiles so far
+  uint32_t s_unit = 0, o_unit = 0;
   uint32_t s_items = 0, o_items = 0;    // items begun
-  while (ok) {
-    // S, one tile ahead
-    while (ok && s_any && st < ot + 2) {
-      if (s_tile == s_end) {
-        s_any = si.next(p);
-        if (!s_any) break;
-        s_tile = si.w.tile0;
-        s_end = si.w.tile1;
-        ok = wait_warp(sb + kQReady, s_items & 1, err);
-        ++s_items;
+  uint32_t t0 = clock();
+  while (true) {
+    if (s_left == 0 && s_any) {
+      s_any = si.next(p);
+      s_left = s_any ? si.w.tile1 - si.w.tile0 : 0;
+      s_first = true;
+      s_items += s_any;
+    }
+    if (o_left == 0) {
+      if (!oi.next(p)) break;
+      o_left = oi.w.tile1 - oi.w.tile0;
+      o_first = true;
+      ++o_items;
+    }
+    uint32_t ready = test_phase(sb + kPFull, ot & 1);
+    ready |= test_phase(sb + kVFull + 8 * o_unit, ot & 1) << 1;
+    ready |= test_phase(sb + kOEmpty, o_items & 1) << 2;               // the item before's (o_items - 2)
+    ready |= test_phase(sb + kSEmpty + 8 * (st & 1), ((st >> 1) & 1) ^ 1u) << 3;
+    ready |= test_phase(sb + kKFull + 8 * s_unit, st & 1) << 4;
+    ready |= test_phase(sb + kQReady, (s_items - 1) & 1) << 5;
+    ready = __reduce_and_sync(0xffffffffu, ready);
+    if (o_unit) ready |= 1u;                       // looked at with the tile's first unit
+    if (o_unit || !o_first || o_items == 1) ready |= 4u;
+    if (s_unit) ready |= 8u;
+    if (s_unit || !s_first) ready |= 32u;
+    if (ot < st && (ready & 7u) == 7u) {
+      if (leader) {
+        tc_fence_after();
+        const uint64_t w = sw128_kmajor_desc(sb + kOffP + o_unit * kBlockBytes);
+        const uint64_t v = sw128_mnmajor_desc(sb + kOffV + o_unit * kVUnitBytes, kBlockBytes);
+        const uint32_t add = o_unit || !o_first;
+        umma_pair<0, 0>(tmem, w, v, kIdescO, add);                      // 16 rows, entries 0 .. 127 of each half
+        umma_pair<0, 2 * kBlockBytes>(tmem + 128, w, v, kIdescO, add);
+        umma_pair<32, 2048>(tmem, w, v, kIdescO, 1);
+        umma_pair<32, 2 * kBlockBytes + 2048>(tmem + 128, w, v, kIdescO, 1);
+        umma_pair<64, 4096>(tmem, w, v, kIdescO, 1);
+        umma_pair<64, 2 * kBlockBytes + 4096>(tmem + 128, w, v, kIdescO, 1);
+        umma_pair<96, 6144>(tmem, w, v, kIdescO, 1);
+        umma_pair<96, 2 * kBlockBytes + 6144>(tmem + 128, w, v, kIdescO, 1);
+        commit_pair(sb + kVEmpty + 8 * o_unit);
+        if (o_unit) commit_pair(sb + kPvDone);
       }
-      const uint32_t place = st & 1;
-      ok = ok && wait_warp(sb + kSEmpty + 8 * place, ((st >> 1) & 1) ^ 1u, err);
-      const uint32_t d = tmem + kTmemS + place * 64;
+      if (o_unit) {
+        ++ot;
+        --o_left;
+        o_first = false;
+      }
+      o_unit ^= 1u;
+      t0 = clock();
+    } else if (s_left && st < ot + 2 && (ready & 56u) == 56u) {
+      if (leader) {
+        tc_fence_after();
+        const uint32_t d = tmem + kTmemS + (st & 1) * 64;
+        uint64_t q = sw128_kmajor_desc(sb + kOffQ + s_unit * kKUnitBytes), k = sw128_kmajor_desc(sb + kOffK + s_unit * kKUnitBytes);
+        uint32_t add = s_unit;
 #pragma unroll 1
-      for (uint32_t u = 0; u < kKUnits && ok; ++u) {
-        ok = wait_warp(sb + kKFull + 8 * u, place, err);
-        if (leader && ok) {
-          tc_fence_after();
-          const uint64_t q = sw128_kmajor_desc(sb + kOffQ + u * 2 * kBlockBytes);
-          const uint64_t k = sw128_kmajor_desc(sb + kOffK + u * 2 * kBlockBytes);
-          umma_pair<0, 0>(d, q, k, kIdescS, u);
+        for (uint32_t b = 0; b < 4 + s_unit; ++b) {
+          umma_pair<0, 0>(d, q, k, kIdescS, add);
           umma_pair<32, 32>(d, q, k, kIdescS, 1);
           umma_pair<64, 64>(d, q, k, kIdescS, 1);
           umma_pair<96, 96>(d, q, k, kIdescS, 1);
-          if (u < 4) {
-            umma_pair<kBlockBytes, kBlockBytes>(d, q, k, kIdescS, 1);
-            umma_pair<kBlockBytes + 32, kBlockBytes + 32>(d, q, k, kIdescS, 1);
-            umma_pair<kBlockBytes + 64, kBlockBytes + 64>(d, q, k, kIdescS, 1);
-            umma_pair<kBlockBytes + 96, kBlockBytes + 96>(d, q, k, kIdescS, 1);
-          }
-          commit_pair(sb + kKEmpty + 8 * u);
+          add = 1;
+          q += kBlockBytes >> 4;
+          k += kBlockBytes >> 4;
+        }
+        commit_pair(sb + kKEmpty + 8 * s_unit);
+        if (s_unit) {
+          commit_pair(sb + kSFull + 8 * (st & 1));
+          if (s_left == 1) commit_pair(sb + kQEmpty);
         }
       }
-      if (leader) commit_pair(sb + kSFull + 8 * place);
-      ++st;
-      if (++s_tile == s_end && leader) commit_pair(sb + kQEmpty);
-    }
-    // O
-    const bool first = o_tile == o_end;
-    if (first) {
-      if (!oi.next(p)) break;
-      o_tile = oi.w.tile0;
-      o_end = oi.w.tile1;
-      if (o_items) ok = ok && wait_warp(sb + kOEmpty, (o_items - 1) & 1, err);
-      ++o_items;
-    }
-    ok = ok && wait_warp(sb + kPFull, ot & 1, err);
-#pragma unroll 1
-    for (uint32_t g = 0; g < kVUnits && ok; ++g) {
-      ok = wait_warp(sb + kVFull + 8 * g, ot & 1, err);
-      if (leader && ok) {
-        tc_fence_after();
-        const uint64_t w = sw128_kmajor_desc(sb + kOffP + (g >> 1) * kBlockBytes + (g & 1) * 64);
-        const uint64_t v = sw128_mnmajor_desc(sb + kOffV + g * kVUnitBytes, kVAtom);
-        const uint32_t add = g || !first;
-        umma_pair<0, 0>(tmem, w, v, kIdescO, add);                        // 16 rows, entries 0 .. 127 of each half
-        umma_pair<0, 2 * kVAtom>(tmem + 128, w, v, kIdescO, add);
-        umma_pair<32, 2048>(tmem, w, v, kIdescO, 1);
-        umma_pair<32, 2 * kVAtom + 2048>(tmem + 128, w, v, kIdescO, 1);
-        commit_pair(sb + kVEmpty + 8 * g);
+      if (s_unit) {
+        ++st;
+        --s_left;
+        s_first = false;
       }
+      s_unit ^= 1u;
+      t0 = clock();
+    } else if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) {
+      record_error(p.a.err, MISA_DEVERR_TIMEOUT);
+      break;
     }
-    if (leader) commit_pair(sb + kPvDone);
-    ++ot;
-    ++o_tile;
+    __syncwarp();
   }
   if (leader) commit_pair(sb + kDone);
   __syncwarp();
@@ -649,11 +636,15 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   if (tid == 0) {
-    constexpr uint32_t kKWriters = kFmt == MISA_KV_BF16 ? 2 : 2 * kKWarps;   // arriving warps of both CTAs
-    constexpr uint32_t kVWriters = kFmt == MISA_KV_BF16 ? 2 : 2 * kVWarps;
-    for (int i = 0; i < kKUnits; ++i) { bar_init(sb + kKFull + 8 * i, kKWriters); bar_init(sb + kKEmpty + 8 * i, 1); }
-    for (int i = 0; i < kVUnits; ++i) { bar_init(sb + kVFull + 8 * i, kVWriters); bar_init(sb + kVEmpty + 8 * i, 1); }
-    for (int i = 0; i < kKUnits + kVUnits; ++i) bar_init(sb + kKLanded + 8 * i, 1);
+    constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 2 : 2 * kRowWarps;   // arriving warps of both CTAs
+    for (int i = 0; i < kUnits; ++i) {
+      bar_init(sb + kKFull + 8 * i, kWriters + (i && kFmt != MISA_KV_BF16 ? 2 : 0));   // and look_ahead
+      bar_init(sb + kVFull + 8 * i, kWriters);
+      bar_init(sb + kKEmpty + 8 * i, 1);
+      bar_init(sb + kVEmpty + 8 * i, 1);
+      bar_init(sb + kKLanded + 8 * i, 1);
+      bar_init(sb + kVLanded + 8 * i, 1);
+    }
     for (int i = 0; i < 2; ++i) { bar_init(sb + kSFull + 8 * i, 1); bar_init(sb + kSEmpty + 8 * i, 8); }
     bar_init(sb + kPFull, 8);
     bar_init(sb + kPvDone, 1);
@@ -690,16 +681,23 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       wait_all(sb, err);   // nothing reads this CTA's memory any more
       __syncwarp();
     } else if (warp == kMmaWarp + 1) {
-      if (elect_one()) ask<kFmt == MISA_KV_BF16>(p, rank, &q_map, &row_map, sb);
+      if (elect_one()) ask_keys<kFmt == MISA_KV_BF16>(p, rank, &q_map, &row_map, sb);
       __syncwarp();
     } else if (warp == kMmaWarp + 2) {
-      pass<kFmt == MISA_KV_BF16>(p, lane, sb);
+      pass_keys<kFmt == MISA_KV_BF16>(p, lane, sb);
+    } else if constexpr (kFmt != MISA_KV_BF16) {
+      look_ahead<kFmt>(p, rank, lane, sb);
+    } else if (warp == kMmaWarp + 3) {
+      if (elect_one()) ask_values(p, rank, &row_map, sb);
+      __syncwarp();
+    } else {
+      pass_values(p, lane, sb);
     }
   } else if (warp >= 4) {
     if constexpr (kFmt != MISA_KV_BF16) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-      if (warp < 4 + kKWarps) bring_keys<kFmt>(p, rank, tid - 128, sb);
-      else bring_values<kFmt>(p, rank, tid - 128 - kKWarps * 32, sb);
+      const bool keys = warp < 4 + kRowWarps;
+      bring_rows<kFmt>(p, rank, keys, tid - (keys ? 128 : 128 + kRowWarps * 32), sb);
     }
   } else {
     if (kFmt != MISA_KV_BF16) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
@@ -960,7 +958,7 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   CUtensorMap rmap = qmap;   // (quantised rows go by plain loads)
   if (a.fmt == MISA_KV_BF16 &&
       !encode_3d_map(&rmap, a.cache, kDqk, static_cast<uint64_t>(a.L), static_cast<uint64_t>(a.nseq), kDqk * 2,
-                     a.nseq > 1 ? static_cast<uint64_t>(a.seq_stride) : static_cast<uint64_t>(a.L) * kDqk * 2, 64, 32))
+                     a.nseq > 1 ? static_cast<uint64_t>(a.seq_stride) : static_cast<uint64_t>(a.L) * kDqk * 2, 64, 64))
     return cudaErrorInvalidValue;
   auto kern = a.fmt == MISA_KV_BF16  ? latent_mla_kernel<MISA_KV_BF16>
               : a.fmt == MISA_KV_MX8 ? latent_mla_kernel<MISA_KV_MX8>
