@@ -13,25 +13,25 @@
 // values, the tensor rate; 48 and 80 cycles where one SM reads both operands).
 //
 // Rows come in tiles of 128.  Per tile:
-//  1. S = Q K^T: CTA u holds rows [64 u, 64 u + 64) of the tile, all 576 entries,
-//     in 9 blocks of 64.  S in TMEM: lane l < 64 has head l against rows 0..63,
-//     lane 64 + l the same head against rows 64..127.
+//  1. CTA u brings rows [64 u, 64 u + 64) of the tile to shared memory as bf16, in 9
+//     blocks of 64 entries: quantised rows widened (exactly) in registers, bf16 rows
+//     by TMA.  S = Q K^T reads these blocks.  S in TMEM: lane l < 64 has head l
+//     against rows 0..63, lane 64 + l the same head against rows 64..127.
 //  2. Softmax in one pass with a running reference m: when a tile's maximum is
 //     more than 2^8 above 2^m, the sums so far are scaled and m moves (p stays
 //     below 2^8, exact enough in bf16 and fp32).  p goes to shared memory as bf16.
-//  3. O += P V: CTA u brings entries [256 u, 256 u + 256) of all 128 rows, 32 rows at
-//     a time (rows of 64 entries in 128-byte swizzled atoms, read MN-major, so
-//     nothing is transposed).  O stays in TMEM, 256 columns.
+//  3. O += P V needs entries [256 u, 256 u + 256) of all 128 rows in CTA u: eight
+//     warps of each CTA copy the blocks it brought to the CTA that multiplies them,
+//     through registers (rows of 64 entries in 128-byte swizzled atoms serve both
+//     products, K-major in one and MN-major in the other).  So a row is read from L2
+//     and widened once.  O stays in TMEM, 256 columns.
 // S has two places, so that the products of tile i + 1 run while the softmax of
-// tile i does.  Quantised rows become bf16 (exactly) on the way from global to
-// shared memory, in registers, the next unit's codes in flight behind; bf16 rows
-// come by TMA.
+// tile i does.
 //
-// What bounds a tile: shared memory, 128 bytes a cycle.  Rows written 139 KB, read
-// 147 KB (S) and 98 KB (O), P 16 KB twice: about 3200 cycles, where the products
-// take 2176 of the tensor cores.  Half of the values are in the other operand
-// already; copying them there, shared memory to shared memory, instead of bringing
-// them twice was slower (3800 cycles a tile for the copies alone).
+// What bounds a tile of bf16 rows is 74 KB a CTA from L2 (about 30 bytes a cycle:
+// 2500 cycles, and all rows twice would be 139 KB) and 32 KB to the other CTA (16
+// bytes a cycle: 2000), of quantised rows the widening as well; the products take
+// 2176 cycles of the tensor cores, the softmax 1500 of its warps.
 //
 // A cluster stays on its SMs and takes every 74th item (a query, or a part of its
 // rows), each role on its own: the rows of the next item come while the output of
@@ -40,13 +40,14 @@
 // items, whose partial sums a second kernel joins in a fixed order.
 //
 // Roles, by warpgroups: warps 0-3 softmax and output (a lane of TMEM each); 8 warps
-// that bring quantised rows for S and 8 for O (none of either for bf16 rows); then
-// one warp that has TMEM and, in the first CTA, issues the MMAs, one that asks for
-// what comes by TMA and one that passes on what has landed.  The softmax holds a
-// tile's 64 scores a lane and more, so the other warpgroups of the large block give
-// it registers.  Shared memory is addressed from one 32-bit base: with a pointer a
-// barrier the kernel spilled, and what shared memory leaves of L1 does not hold the
-// stack.  Waits are bounded.
+// that bring quantised rows (none for bf16); 8 that copy; then one warp that has TMEM
+// and, in the first CTA, issues the MMAs, and one or two that ask for what comes by
+// TMA and pass on what has landed.  The softmax holds a tile's 64 scores a lane and
+// more, so the other warpgroups give it registers.  Shared memory is addressed from
+// one 32-bit base: with a pointer a barrier the kernel spilled, and what shared
+// memory leaves of L1 does not hold the stack.  Code is kept small (loops, not
+// copies): at 140 KB the instruction caches, which many SMs share, halved the speed.
+// Waits are bounded.
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"
@@ -73,9 +74,10 @@ constexpr uint32_t kKFull = kOffBar;              // [2] first CTA: unit brought
 constexpr uint32_t kVFull = kKFull + 16;          // [2] first CTA
 constexpr uint32_t kKEmpty = kVFull + 16;         // [2] multiplied
 constexpr uint32_t kVEmpty = kKEmpty + 16;        // [2]
-constexpr uint32_t kKLanded = kVEmpty + 16;       // [2] bf16: TMA done
-constexpr uint32_t kVLanded = kKLanded + 16;      // [2]
-constexpr uint32_t kSFull = kVLanded + 16;   // [2] S complete
+constexpr uint32_t kKHere = kVEmpty + 16;         // [2] brought by this CTA (bf16: landed)
+constexpr uint32_t kCopied = kKHere + 16;         // [2] read by those that copy to O's operand
+constexpr uint32_t kVLanded = kCopied + 16;       // this CTA's values of the other one's rows
+constexpr uint32_t kSFull = kVLanded + 8;   // [2] S complete
 constexpr uint32_t kSEmpty = kSFull + 16;         // [2] first CTA: S read by both
 constexpr uint32_t kPFull = kSEmpty + 16;         // first CTA: P written (and O scaled) by both
 constexpr uint32_t kPvDone = kPFull + 8;          // O += P V complete
@@ -88,10 +90,10 @@ constexpr uint32_t kOffTmem = kDone + 8;
 constexpr uint32_t kOffRed = (kOffTmem + 8 + 15) / 16 * 16;   // [3][128] floats
 constexpr int kSmemBytes = kOffRed + 3 * 128 * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-// Warps: 0-3 softmax and output, then those that bring quantised rows, then four more.
-constexpr int kRowWarps = 8;   // for S, and as many for O
-constexpr int first_other_warp(int fmt) { return fmt == MISA_KV_BF16 ? 4 : 4 + 2 * kRowWarps; }
-constexpr int block_threads(int fmt) { return (first_other_warp(fmt) + (fmt == MISA_KV_BF16 ? 5 : 4)) * 32; }
+// Warps: 0-3 softmax and output, those that bring quantised rows, those that copy, four more.
+constexpr int kRowWarps = 8, kCopyWarps = 8;
+constexpr int first_copy_warp(int fmt) { return fmt == MISA_KV_BF16 ? 4 : 4 + kRowWarps; }
+constexpr int block_threads(int fmt) { return (first_copy_warp(fmt) + kCopyWarps + 4) * 32; }
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 64 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -99,6 +101,9 @@ constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values 
 // ---------------------------------------------------------------- shared memory by address
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void arrive_here(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -113,6 +118,18 @@ __device__ __forceinline__ void arrive_in(uint32_t bar, uint32_t rank) {
       "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar),
       "r"(rank)
       : "memory");
+}
+// The address of the same place in CTA `rank`, and a 16-byte store there that a
+// barrier of that CTA counts.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_async16(uint32_t remote, uint4 v, uint32_t remote_bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote),
+               "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(remote_bar)
+               : "memory");
 }
 // Whether the phase of `parity` is over (try: may sleep a while first).
 __device__ __forceinline__ uint32_t test_phase(uint32_t bar, uint32_t parity) {
@@ -343,25 +360,15 @@ __device__ __forceinline__ uint2 load_code(const uint8_t* row, int entry) {   //
   return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row + entry / 2)), 0u);
 }
 
-// Signals a unit: this lane's writes are visible to the tensor core, and the warp
-// arrives once.
-__device__ __forceinline__ void unit_ready(uint32_t full) {
-  fence_proxy_async_smem();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) arrive_in(full, 0);
-}
-
-// Brings quantised rows, 256 threads for S and 256 for O (the same code, for the
-// instruction caches' sake): thread = (rows r0 and r0 + 32, piece of 8 entries) of
-// each of a unit's four blocks.  An absent row is any row's codes with scales of
-// zero.  Where a piece has been widened, the same piece of the next unit is asked
-// for into its registers.
+// Brings quantised rows, 256 threads: thread = (rows r0 and r0 + 32, piece of 8
+// entries) of each of a unit's four blocks.  An absent row is any row's codes with
+// scales of zero.  Where a piece has been widened, the same piece of the next unit
+// is asked for into its registers.
 template <int kFmt>
-__device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, bool keys, int tid, uint32_t sb) {
+__device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7;
-  const uint32_t dst0 = sb + (keys ? kOffK : kOffV) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 32 apart: the same swizzle
-  const uint32_t full = sb + (keys ? kKFull : kVFull), empty = sb + (keys ? kKEmpty : kVEmpty);
+  const uint32_t dst0 = sb + kOffK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 32 apart: the same swizzle
   const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
   uint32_t parity = 1;
   for (Items it(p); it.next(p);) {
@@ -369,10 +376,9 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, bo
     const int begin = w.tile0 * kUnits, end = w.tile1 * kUnits;   // units are counted over the tiles
     int32_t id[2];
     auto load_ids = [&](int unit) {
-      const int first = keys ? (unit >> 1) * kTile + static_cast<int>(rank) * 64 : unit * 64;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int s = first + r0 + 32 * i;
+        const int s = (unit >> 1) * kTile + static_cast<int>(rank) * 64 + r0 + 32 * i;
         id[i] = unit < end && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
       }
     };
@@ -384,12 +390,12 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, bo
     for (int unit = begin - 1; unit < end; ++unit) {
       const uint32_t u = unit & 1, next = u ^ 1u;
       const bool real = unit >= begin;
-      if (real && !wait_warp(empty + 8 * u, parity, p.a.err)) return;
+      if (real && !(wait_warp(sb + kKEmpty + 8 * u, parity, p.a.err) && wait_warp(sb + kCopied + 8 * u, parity, p.a.err))) return;
       const uint32_t dst = dst0 + u * kKUnitBytes;
-      const int entry = (keys ? static_cast<int>(next) : static_cast<int>(rank)) * 256;   // of the next unit
+      const int entry = static_cast<int>(next) * 256;   // of the next unit
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (keys && piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(p.a.err, MISA_DEVERR_BAD_INDEX);
+        if (piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(p.a.err, MISA_DEVERR_BAD_INDEX);
         const bool here = id[i] >= 0 && id[i] < w.L;
         const uint8_t* src = w.base + static_cast<int64_t>(here ? id[i] : 0) * kRow;
 #pragma unroll
@@ -401,7 +407,7 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, bo
         }
         scale[i] = make_uint2(0u, 0u);
         if (here) scale[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + (entry >> 5)));
-        if (keys && u) {   // the rotary block, and the next tile's asked for
+        if (u) {   // the rotary block, and the next tile's asked for
           if (real) st_shared16(dst + 4 * kBlockBytes + i * 4096, rope[i]);
           rope[i] = make_uint4(0u, 0u, 0u, 0u);
           if (here) rope[i] = __ldg(reinterpret_cast<const uint4*>(src + kv_rope_offset(kFmt) + piece * 16));
@@ -409,21 +415,95 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, bo
       }
       load_ids(unit + 2);
       if (real) {
-        unit_ready(full + 8 * u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+          arrive_here(sb + kKHere + 8 * u);
+          arrive_in(sb + kKFull + 8 * u, 0);
+        }
         parity ^= u;
       }
     }
   }
 }
 
-// Asks the quantised rows of the tile after the next into L2, a warp: in a prefix one
-// request for the CTA's 64 rows, else line by line.
+// Copies this CTA's rows, 256 threads as in bring_rows, to O's operand: entries
+// 0 .. 255 to the first CTA, the others to the second, in each as the unit of this
+// CTA's rows.  What goes to the other CTA is counted there.  Absent rows of a bf16
+// cache are cleared: P is 0 there, but 0 times a stale NaN is not.
 template <int kFmt>
-__device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, int lane, uint32_t sb) {
+__device__ __forceinline__ void copy_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
+  const int r0 = tid >> 3, piece = tid & 7;
+  const uint32_t off = r0 * 128 + ((piece ^ (r0 & 7)) << 4);
+  const uint32_t src0 = sb + kOffK + off, dst = sb + kOffV + rank * kVUnitBytes + off;
+  const uint32_t far = in_cta(dst, rank ^ 1u), far_bar = in_cta(sb + kVLanded, rank ^ 1u);
+  uint32_t parity = 0;
+  for (Items it(p); it.next(p);)
+#pragma unroll 1
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
+      const int row = tile * kTile + static_cast<int>(rank) * 64 + r0;
+#pragma unroll 1
+      for (uint32_t turn = 0; turn < 2; ++turn) {
+        const uint32_t u = rank ^ 1u ^ turn;   // the other CTA's first: it takes longer
+        if (!wait_warp(sb + kKHere + 8 * u, parity, p.a.err)) return;
+        uint4 y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = ld_shared16(src0 + u * kKUnitBytes + (i & 3) * kBlockBytes + (i >> 2) * 4096);
+          if (kFmt == MISA_KV_BF16 && row + (i >> 2) * 32 >= it.w.n) y[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();   // read before TMA may write there again
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) arrive_here(sb + kCopied + 8 * u);
+        if (turn == 0 && !wait_warp(sb + kVEmpty + 8 * rank, parity ^ 1u, p.a.err)) return;
+        if (u == rank) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) st_shared16(dst + (i & 3) * kBlockBytes + (i >> 2) * 4096, y[i]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + 8 * rank, 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) st_async16(far + (i & 3) * kBlockBytes + (i >> 2) * 4096, y[i], far_bar);
+        }
+      }
+    }
+}
+// Passes on to the first CTA what the other one has copied here, a warp.
+__device__ __forceinline__ void pass_copies(const MlaParams& p, uint32_t rank, int lane, uint32_t sb) {
+  uint32_t parity = 0;
+  if (lane == 0) bar_expect(sb + kVLanded, kVUnitBytes);
+  for (Items it(p); it.next(p);)
+#pragma unroll 1
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
+      if (!wait_warp(sb + kVLanded, parity, p.a.err)) return;
+      if (lane == 0) {
+        bar_expect(sb + kVLanded, kVUnitBytes);
+        asm volatile("fence.proxy.async;" ::: "memory");
+        arrive_in(sb + kVFull + 8 * (rank ^ 1u), 0);
+      }
+    }
+}
+
+// Brings the queries of this CTA's heads and asks the quantised rows of the tile
+// after the next into L2, a warp: in a prefix one request for the CTA's 64 rows,
+// else line by line.
+template <int kFmt>
+__device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, int lane, const CUtensorMap* q_map, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
-  uint32_t parity = 1;
-  for (Items it(p); it.next(p);) {
+  uint32_t parity = 1, items = 0;
+  for (Items it(p); it.next(p); ++items) {
     const Work& w = it.w;
+    if (!wait_warp(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
+    if (elect_one()) {
+      bar_expect(sb + kQFull, kBlocks * kBlockBytes);
+#pragma unroll 1
+      for (int b = 0; b < kBlocks; ++b)
+        tma_2d(sb + kOffQ + b * kBlockBytes, q_map, sb + kQFull, b * 64, w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
+    }
+    __syncwarp();
+    if (!wait_warp(sb + kQFull, items & 1, p.a.err)) return;
+    if (lane == 0) arrive_in(sb + kQReady, 0);
     for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u) {
       // Goes on with the tiles: S of this one waits for the arrival, so that no phase
       // can pass by unseen.
@@ -450,10 +530,8 @@ __device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, in
   }
 }
 
-// Brings the queries of this CTA's heads and, of a bf16 cache, the rows for S, by
-// TMA; one thread.
-template <bool kRows>
-__device__ __forceinline__ void ask_keys(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
+// Of a bf16 cache, brings queries and rows by TMA; one thread.
+__device__ __forceinline__ void ask_rows(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
   uint32_t items = 0, parity = 1;
   for (Items it(p); it.next(p); ++items) {
     if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
@@ -461,70 +539,35 @@ __device__ __forceinline__ void ask_keys(const MlaParams& p, uint32_t rank, cons
 #pragma unroll 1
     for (int b = 0; b < kBlocks; ++b)
       tma_2d(sb + kOffQ + b * kBlockBytes, q_map, sb + kQFull, b * 64, it.w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
-    for (int tile = it.w.tile0; kRows && tile < it.w.tile1; ++tile, parity ^= 1u) {
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
       const int row = tile * kTile + static_cast<int>(rank) * 64;
 #pragma unroll 1
       for (int b = 0; b < kBlocks; ++b) {
         const uint32_t u = b >= 4;
         if ((b & 3) == 0 && b < 8) {
-          if (!wait_one(sb + kKEmpty + 8 * u, parity, p.a.err)) return;
-          bar_expect(sb + kKLanded + 8 * u, (u ? 5 : 4) * kBlockBytes);
+          if (!wait_one(sb + kKEmpty + 8 * u, parity, p.a.err) || !wait_one(sb + kCopied + 8 * u, parity, p.a.err)) return;
+          bar_expect(sb + kKHere + 8 * u, (u ? 5 : 4) * kBlockBytes);
         }
-        tma_3d(sb + kOffK + b * kBlockBytes, map, sb + kKLanded + 8 * u, b * 64, row, it.w.seq);
+        tma_3d(sb + kOffK + b * kBlockBytes, map, sb + kKHere + 8 * u, b * 64, row, it.w.seq);
         if (tile + 2 < it.w.tile1) tma_l2_3d(map, b * 64, row + 2 * kTile, it.w.seq);   // two tiles ahead into L2
       }
     }
   }
 }
-// The same for O's rows.
-__device__ __forceinline__ void ask_values(const MlaParams& p, uint32_t rank, const CUtensorMap* map, uint32_t sb) {
-  uint32_t parity = 1;
-  for (Items it(p); it.next(p);)
-#pragma unroll 1
-    for (int unit = it.w.tile0 * kUnits; unit < it.w.tile1 * kUnits; ++unit) {
-      const uint32_t g = unit & 1;
-      if (!wait_one(sb + kVEmpty + 8 * g, parity, p.a.err)) return;
-      bar_expect(sb + kVLanded + 8 * g, kVUnitBytes);
-#pragma unroll 1
-      for (int a = 0; a < 4; ++a)
-        tma_3d(sb + kOffV + g * kVUnitBytes + a * kBlockBytes, map, sb + kVLanded + 8 * g, static_cast<int>(rank) * 256 + a * 64,
-               unit * 64, it.w.seq);
-      parity ^= g;
-    }
-}
-// Pass on to the first CTA what has landed, a warp each.
-template <bool kRows>
-__device__ __forceinline__ void pass_keys(const MlaParams& p, int lane, uint32_t sb) {
+// Passes on to the first CTA what has landed, one thread.
+__device__ __forceinline__ void pass_rows(const MlaParams& p, uint32_t sb) {
   uint32_t items = 0, parity = 0;
   for (Items it(p); it.next(p); ++items) {
-    if (!wait_warp(sb + kQFull, items & 1, p.a.err)) return;
-    if (lane == 0) arrive_in(sb + kQReady, 0);
+    if (!wait_one(sb + kQFull, items & 1, p.a.err)) return;
+    arrive_in(sb + kQReady, 0);
 #pragma unroll 1
-    for (int unit = it.w.tile0 * kUnits; kRows && unit < it.w.tile1 * kUnits; ++unit) {
+    for (int unit = it.w.tile0 * kUnits; unit < it.w.tile1 * kUnits; ++unit) {
       const uint32_t u = unit & 1;
-      if (!wait_warp(sb + kKLanded + 8 * u, parity, p.a.err)) return;
-      if (lane == 0) arrive_in(sb + kKFull + 8 * u, 0);
+      if (!wait_one(sb + kKHere + 8 * u, parity, p.a.err)) return;
+      arrive_in(sb + kKFull + 8 * u, 0);
       parity ^= u;
     }
   }
-}
-// Rows behind the prefix are cleared: P is 0 there, but 0 times a stale NaN is not.
-__device__ __forceinline__ void pass_values(const MlaParams& p, int lane, uint32_t sb) {
-  uint32_t parity = 0;
-  for (Items it(p); it.next(p);)
-#pragma unroll 1
-    for (int unit = it.w.tile0 * kUnits; unit < it.w.tile1 * kUnits; ++unit) {
-      const uint32_t g = unit & 1;
-      if (!wait_warp(sb + kVLanded + 8 * g, parity, p.a.err)) return;
-      const int live = min(max(it.w.n - unit * 64, 0), 64);
-#pragma unroll 1
-      for (int a = 0; a < 4; ++a)
-#pragma unroll 1
-        for (int c = live * 8 + lane; c < 64 * 8; c += 32)   // whole rows: the swizzle does not matter
-          st_shared16(sb + kOffV + g * kVUnitBytes + a * kBlockBytes + c * 16, make_uint4(0u, 0u, 0u, 0u));
-      unit_ready(sb + kVFull + 8 * g);
-      parity ^= g;
-    }
 }
 
 // Issues the products of both CTAs, a warp of the first.  Two rows of work over the
@@ -632,19 +675,20 @@ __global__ void __launch_bounds__(block_threads(kFmt), 1) __cluster_dims__(2, 1,
 latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap row_map, const MlaParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  constexpr int kMmaWarp = first_other_warp(kFmt);
+  constexpr int kMmaWarp = first_copy_warp(kFmt) + kCopyWarps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   if (tid == 0) {
-    constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 2 : 2 * kRowWarps;   // arriving warps of both CTAs
+    constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 1 : kRowWarps;   // that arrive in a CTA
     for (int i = 0; i < kUnits; ++i) {
-      bar_init(sb + kKFull + 8 * i, kWriters + (i && kFmt != MISA_KV_BF16 ? 2 : 0));   // and look_ahead
-      bar_init(sb + kVFull + 8 * i, kWriters);
+      bar_init(sb + kKFull + 8 * i, 2 * kWriters + (i && kFmt != MISA_KV_BF16 ? 2 : 0));   // and look_ahead
+      bar_init(sb + kKHere + 8 * i, kWriters);
       bar_init(sb + kKEmpty + 8 * i, 1);
+      bar_init(sb + kCopied + 8 * i, kCopyWarps);
+      bar_init(sb + kVFull + 8 * i, kCopyWarps + 1);   // of the CTA whose rows they are, and pass_copies of the other
       bar_init(sb + kVEmpty + 8 * i, 1);
-      bar_init(sb + kKLanded + 8 * i, 1);
-      bar_init(sb + kVLanded + 8 * i, 1);
     }
+    bar_init(sb + kVLanded, 1);
     for (int i = 0; i < 2; ++i) { bar_init(sb + kSFull + 8 * i, 1); bar_init(sb + kSEmpty + 8 * i, 8); }
     bar_init(sb + kPFull, 8);
     bar_init(sb + kPvDone, 1);
@@ -673,34 +717,40 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 
   const LatentArgs& a = p.a;
   uint32_t* err = a.err;
-  // (768 threads of 80 registers: 152 + 4 * 64 + 72 of 480 for the six warpgroups)
+  // Registers of the warpgroups: 152 + 2 * 64 + 2 * 64 + 72 of 6 * 80, or 168 + 2 * 112 + 120 of 4 * 128
+  constexpr bool kQuant = kFmt != MISA_KV_BF16;
   if (warp >= kMmaWarp) {
-    if (kFmt != MISA_KV_BF16) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     if (warp == kMmaWarp) {
       if (rank == 0) multiply(p, tmem, sb);
       wait_all(sb, err);   // nothing reads this CTA's memory any more
       __syncwarp();
     } else if (warp == kMmaWarp + 1) {
-      if (elect_one()) ask_keys<kFmt == MISA_KV_BF16>(p, rank, &q_map, &row_map, sb);
-      __syncwarp();
+      if constexpr (kQuant) {
+        look_ahead<kFmt>(p, rank, lane, &q_map, sb);
+      } else {
+        if (elect_one()) ask_rows(p, rank, &q_map, &row_map, sb);
+        __syncwarp();
+      }
     } else if (warp == kMmaWarp + 2) {
-      pass_keys<kFmt == MISA_KV_BF16>(p, lane, sb);
-    } else if constexpr (kFmt != MISA_KV_BF16) {
-      look_ahead<kFmt>(p, rank, lane, sb);
-    } else if (warp == kMmaWarp + 3) {
-      if (elect_one()) ask_values(p, rank, &row_map, sb);
+      pass_copies(p, rank, lane, sb);
+    } else if constexpr (!kQuant) {
+      if (elect_one()) pass_rows(p, sb);
       __syncwarp();
-    } else {
-      pass_values(p, lane, sb);
     }
+  } else if (warp >= first_copy_warp(kFmt)) {
+    if (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    copy_rows<kFmt>(p, rank, tid - first_copy_warp(kFmt) * 32, sb);
   } else if (warp >= 4) {
-    if constexpr (kFmt != MISA_KV_BF16) {
+    if constexpr (kQuant) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-      const bool keys = warp < 4 + kRowWarps;
-      bring_rows<kFmt>(p, rank, keys, tid - (keys ? 128 : 128 + kRowWarps * 32), sb);
+      bring_rows<kFmt>(p, rank, tid - 128, sb);
     }
   } else {
-    if (kFmt != MISA_KV_BF16) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    if (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ------------------------------------------------------------ softmax and output
     const int half = warp >> 1;                     // rows [64 half, 64 half + 64) of a tile, entries 256 half .. of O
     const int hl = (warp & 1) * 32 + lane;          // head of this CTA
