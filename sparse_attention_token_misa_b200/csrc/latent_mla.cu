@@ -57,45 +57,45 @@ namespace misa {
 namespace {
 
 constexpr int kDqk = MISA_MLA_DQK, kDv = MISA_MLA_DV;
-constexpr int kTile = 128;                        // rows of a tile
+constexpr int kTile = 64;                         // rows of a tile
+constexpr int kRows = 32;                         // ... that one CTA brings
 constexpr int kHeads = 64;                        // heads of a CTA
 constexpr int kBlocks = kDqk / 64;                // 9
-constexpr uint32_t kBlockBytes = 64 * 128;        // 64 rows (heads) x 64 bf16
-constexpr int kUnits = 2;                         // both operands are brought and freed by halves:
-constexpr uint32_t kKUnitBytes = 4 * kBlockBytes; // S: blocks 0..3 and 4..8 of the CTA's 64 rows
-constexpr uint32_t kVUnitBytes = 4 * kBlockBytes; // O: 256 entries of rows 0..63 and 64..127
+constexpr uint32_t kQBlock = kHeads * 128;        // 64 heads x 64 entries
+constexpr uint32_t kKBlock = kRows * 128;         // 32 rows x 64 entries
+constexpr uint32_t kVBlock = kTile * 128;         // 64 rows x 64 entries
+constexpr uint32_t kKStage = kBlocks * kKBlock;   // S operand: the CTA's rows
+constexpr uint32_t kVStage = 4 * kVBlock;         // O operand: 256 entries of all rows
+constexpr uint32_t kPStage = kHeads * 128;
 constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = kOffQ + kBlocks * kBlockBytes;
-constexpr uint32_t kOffV = kOffK + kBlocks * kBlockBytes;
-constexpr uint32_t kOffP = kOffV + kUnits * kVUnitBytes;
-constexpr uint32_t kOffBar = kOffP + 2 * kBlockBytes;
-// barriers (of the first CTA where it says so)
-constexpr uint32_t kKFull = kOffBar;              // [2] first CTA: unit brought by both
-constexpr uint32_t kVFull = kKFull + 16;          // [2] first CTA
-constexpr uint32_t kKEmpty = kVFull + 16;         // [2] multiplied
-constexpr uint32_t kVEmpty = kKEmpty + 16;        // [2]
-constexpr uint32_t kKHere = kVEmpty + 16;         // [2] brought by this CTA (bf16: landed)
-constexpr uint32_t kCopied = kKHere + 16;         // [2] read by those that copy to O's operand
-constexpr uint32_t kVLanded = kCopied + 16;       // this CTA's values of the other one's rows
-constexpr uint32_t kSFull = kVLanded + 8;   // [2] S complete
-constexpr uint32_t kSEmpty = kSFull + 16;         // [2] first CTA: S read by both
+constexpr uint32_t kOffK = kOffQ + kBlocks * kQBlock;   // [2]: stage = a tile's number modulo 2
+constexpr uint32_t kOffV = kOffK + 2 * kKStage;         // [2]
+constexpr uint32_t kOffP = kOffV + 2 * kVStage;         // [2]
+// barriers, one a stage (of the first CTA where it says so)
+constexpr uint32_t kKFull = kOffP + 2 * kPStage;  // first CTA: rows brought by both
+constexpr uint32_t kKHere = kKFull + 16;          // bf16: this CTA's rows landed
+constexpr uint32_t kKEmpty = kKHere + 16;         // multiplied
+constexpr uint32_t kCopied = kKEmpty + 16;        // bf16: read by those that copy to O's operand
+constexpr uint32_t kVFull = kCopied + 16;         // first CTA: both CTAs' values are there
+constexpr uint32_t kVLanded = kVFull + 16;        // this CTA's values of the other one's rows
+constexpr uint32_t kVEmpty = kVLanded + 16;       // multiplied
+constexpr uint32_t kSFull = kVEmpty + 16;         // S complete
+constexpr uint32_t kSEmpty = kSFull + 16;         // first CTA: S read by both
 constexpr uint32_t kPFull = kSEmpty + 16;         // first CTA: P written (and O scaled) by both
-constexpr uint32_t kPvDone = kPFull + 8;          // O += P V complete
-constexpr uint32_t kOEmpty = kPvDone + 8;         // first CTA: O of the item before read by both
-constexpr uint32_t kQFull = kOEmpty + 8;          // this CTA's queries landed
-constexpr uint32_t kQReady = kQFull + 8;          // first CTA: both CTAs' queries landed
-constexpr uint32_t kQEmpty = kQReady + 8;         // the item's last S complete
-constexpr uint32_t kDone = kQEmpty + 8;           // every MMA retired
+constexpr uint32_t kPvDone = kPFull + 16;         // O += P V complete
+constexpr uint32_t kOEmpty = kPvDone + 16;        // (one) first CTA: O of the item before read by both
+constexpr uint32_t kQFull = kOEmpty + 8;          // (one) this CTA's queries landed
+constexpr uint32_t kQReady = kQFull + 8;          // (one) first CTA: both CTAs' queries landed
+constexpr uint32_t kQEmpty = kQReady + 8;         // (one) the item's last S complete
+constexpr uint32_t kDone = kQEmpty + 8;           // (one) every MMA retired
 constexpr uint32_t kOffTmem = kDone + 8;
 constexpr uint32_t kOffRed = (kOffTmem + 8 + 15) / 16 * 16;   // [3][128] floats
 constexpr int kSmemBytes = kOffRed + 3 * 128 * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-// Warps: 0-3 softmax and output, those that bring quantised rows, those that copy, four more.
-constexpr int kRowWarps = 8, kCopyWarps = 8;
-constexpr int first_copy_warp(int fmt) { return fmt == MISA_KV_BF16 ? 4 : 4 + kRowWarps; }
-constexpr int block_threads(int fmt) { return (first_copy_warp(fmt) + kCopyWarps + 4) * 32; }
-constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 64 columns
-constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128);
+// Warps: 0-3 softmax and output, 4-11 bring quantised rows or copy bf16 ones, 12-15 the rest.
+constexpr int kRowWarps = 8, kMmaWarp = 4 + kRowWarps, kThreads = (kMmaWarp + 4) * 32;
+constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 32 columns
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 64);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
 
 // ---------------------------------------------------------------- shared memory by address
@@ -360,227 +360,223 @@ __device__ __forceinline__ uint2 load_code(const uint8_t* row, int entry) {   //
   return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row + entry / 2)), 0u);
 }
 
-// Brings quantised rows, 256 threads: thread = (rows r0 and r0 + 32, piece of 8
-// entries) of each of a unit's four blocks.  An absent row is any row's codes with
-// scales of zero.  Where a piece has been widened, the same piece of the next unit
-// is asked for into its registers.
+// A tile's number over all items of the cluster: its stage and its phase there.
+struct Turn {
+  uint32_t n = 0;
+  __device__ __forceinline__ uint32_t at() const { return 8 * (n & 1); }        // its barrier of two
+  __device__ __forceinline__ uint32_t stage() const { return n & 1; }
+  __device__ __forceinline__ uint32_t parity() const { return (n >> 1) & 1; }   // of the phase that ends with this tile
+  __device__ __forceinline__ uint32_t before() const { return parity() ^ 1u; }  // of the one that ended two tiles ago
+};
+
+// Brings quantised rows, 256 threads: thread = (row r0, piece of 8 entries) of each
+// block.  A piece is widened once and written twice: to S's operand, and to O's in
+// the CTA that multiplies it.  An absent row is any row's codes with scales of zero.
+// Where a piece has been widened, the same piece of the next tile is asked for into
+// its registers.
 template <int kFmt>
 __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
-  const int r0 = tid >> 3, piece = tid & 7;
-  const uint32_t dst0 = sb + kOffK + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // rows 32 apart: the same swizzle
+  const int r0 = tid >> 3, piece = tid & 7, own = static_cast<int>(rank) * kRows + r0;
+  const uint32_t turn = (piece ^ (r0 & 7)) << 4;
+  const uint32_t kdst0 = sb + kOffK + r0 * 128 + turn, vdst0 = sb + kOffV + own * 128 + turn;
+  const uint32_t far0 = in_cta(vdst0, rank ^ 1u), far_bar0 = in_cta(sb + kVLanded, rank ^ 1u);
   const uint32_t sel = 0x4440u | (piece >> 2);   // the piece's byte of a block's two scale bytes
-  uint32_t parity = 1;
+  Turn n;
   for (Items it(p); it.next(p);) {
     const Work& w = it.w;
-    const int begin = w.tile0 * kUnits, end = w.tile1 * kUnits;   // units are counted over the tiles
-    int32_t id[2];
-    auto load_ids = [&](int unit) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int s = (unit >> 1) * kTile + static_cast<int>(rank) * 64 + r0 + 32 * i;
-        id[i] = unit < end && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
-      }
+    int32_t id;
+    auto load_id = [&](int tile) {
+      const int s = tile * kTile + own;
+      id = tile < w.tile1 && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
     };
-    uint2 code[8], scale[2];
-    uint4 rope[2];
-    load_ids(begin);
-    // The first turn only asks for the first unit.
+    uint2 code[8];
+    uint4 scale, rope;
+    load_id(w.tile0);
+    // The first turn only asks for the first tile.
 #pragma unroll 1
-    for (int unit = begin - 1; unit < end; ++unit) {
-      const uint32_t u = unit & 1, next = u ^ 1u;
-      const bool real = unit >= begin;
-      if (real && !(wait_warp(sb + kKEmpty + 8 * u, parity, p.a.err) && wait_warp(sb + kCopied + 8 * u, parity, p.a.err))) return;
-      const uint32_t dst = dst0 + u * kKUnitBytes;
-      const int entry = static_cast<int>(next) * 256;   // of the next unit
+    for (int tile = w.tile0 - 1; tile < w.tile1; ++tile) {
+      const bool real = tile >= w.tile0;
+      if (real && !(wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err) && wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)))
+        return;
+      if (piece == 0 && (id < -1 || id >= w.L)) record_error(p.a.err, MISA_DEVERR_BAD_INDEX);
+      const bool here = id >= 0 && id < w.L;
+      const uint8_t* src = w.base + static_cast<int64_t>(here ? id : 0) * kRow;   // of the next tile
+      const uint32_t kdst = kdst0 + n.stage() * kKStage, vofs = n.stage() * kVStage, far_bar = far_bar0 + n.at();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (piece == 0 && (id[i] < -1 || id[i] >= w.L)) record_error(p.a.err, MISA_DEVERR_BAD_INDEX);
-        const bool here = id[i] >= 0 && id[i] < w.L;
-        const uint8_t* src = w.base + static_cast<int64_t>(here ? id[i] : 0) * kRow;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint4 y = kv_decode8<kFmt>(code[i * 4 + b].x, code[i * 4 + b].y,
-                                           kv_scale(__byte_perm(b < 2 ? scale[i].x : scale[i].y, 0u, sel + 2 * (b & 1))));
-          if (real) st_shared16(dst + b * kBlockBytes + i * 4096, y);
-          code[i * 4 + b] = load_code<kFmt>(src, entry + b * 64 + piece * 8);
+      for (int b = 0; b < 8; ++b) {
+        const uint32_t word = b < 2 ? scale.x : b < 4 ? scale.y : b < 6 ? scale.z : scale.w;
+        const uint4 y = kv_decode8<kFmt>(code[b].x, code[b].y, kv_scale(__byte_perm(word, 0u, sel + 2 * (b & 1))));
+        if (real) {
+          st_shared16(kdst + b * kKBlock, y);
+          if ((b >> 2) == static_cast<int>(rank)) st_shared16(vdst0 + vofs + (b & 3) * kVBlock, y);
+          else st_async16(far0 + vofs + (b & 3) * kVBlock, y, far_bar);
         }
-        scale[i] = make_uint2(0u, 0u);
-        if (here) scale[i] = __ldg(reinterpret_cast<const uint2*>(src + kv_code_bytes(kFmt) + (entry >> 5)));
-        if (u) {   // the rotary block, and the next tile's asked for
-          if (real) st_shared16(dst + 4 * kBlockBytes + i * 4096, rope[i]);
-          rope[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (here) rope[i] = __ldg(reinterpret_cast<const uint4*>(src + kv_rope_offset(kFmt) + piece * 16));
-        }
+        code[b] = load_code<kFmt>(src, b * 64 + piece * 8);
       }
-      load_ids(unit + 2);
+      if (real) st_shared16(kdst + 8 * kKBlock, rope);
+      scale = rope = make_uint4(0u, 0u, 0u, 0u);
+      if (here) {
+        scale = __ldg(reinterpret_cast<const uint4*>(src + kv_code_bytes(kFmt)));
+        rope = __ldg(reinterpret_cast<const uint4*>(src + kv_rope_offset(kFmt) + piece * 16));
+      }
+      load_id(tile + 2);
       if (real) {
         fence_proxy_async_smem();
         __syncwarp();
         if ((threadIdx.x & 31) == 0) {
-          arrive_here(sb + kKHere + 8 * u);
-          arrive_in(sb + kKFull + 8 * u, 0);
+          arrive_in(sb + kKFull + n.at(), 0);
+          arrive_in(sb + kVFull + n.at(), 0);
         }
-        parity ^= u;
+        ++n.n;
       }
     }
   }
 }
 
-// Copies this CTA's rows, 256 threads as in bring_rows, to O's operand: entries
-// 0 .. 255 to the first CTA, the others to the second, in each as the unit of this
-// CTA's rows.  What goes to the other CTA is counted there.  Absent rows of a bf16
-// cache are cleared: P is 0 there, but 0 times a stale NaN is not.
-template <int kFmt>
+// Copies this CTA's rows of a bf16 cache, 256 threads as above, to O's operand.
+// Absent rows are cleared: P is 0 there, but 0 times a stale NaN is not.
 __device__ __forceinline__ void copy_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
-  const int r0 = tid >> 3, piece = tid & 7;
-  const uint32_t off = r0 * 128 + ((piece ^ (r0 & 7)) << 4);
-  const uint32_t src0 = sb + kOffK + off, dst = sb + kOffV + rank * kVUnitBytes + off;
-  const uint32_t far = in_cta(dst, rank ^ 1u), far_bar = in_cta(sb + kVLanded, rank ^ 1u);
-  uint32_t parity = 0;
+  const int r0 = tid >> 3, piece = tid & 7, own = static_cast<int>(rank) * kRows + r0;
+  const uint32_t turn = (piece ^ (r0 & 7)) << 4;
+  const uint32_t src0 = sb + kOffK + r0 * 128 + turn, vdst0 = sb + kOffV + own * 128 + turn;
+  const uint32_t far0 = in_cta(vdst0, rank ^ 1u), far_bar0 = in_cta(sb + kVLanded, rank ^ 1u);
+  Turn n;
   for (Items it(p); it.next(p);)
 #pragma unroll 1
-    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
-      const int row = tile * kTile + static_cast<int>(rank) * 64 + r0;
-#pragma unroll 1
-      for (uint32_t turn = 0; turn < 2; ++turn) {
-        const uint32_t u = rank ^ 1u ^ turn;   // the other CTA's first: it takes longer
-        if (!wait_warp(sb + kKHere + 8 * u, parity, p.a.err)) return;
-        uint4 y[8];
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
+      if (!wait_warp(sb + kKHere + n.at(), n.parity(), p.a.err)) return;
+      uint4 y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = ld_shared16(src0 + u * kKUnitBytes + (i & 3) * kBlockBytes + (i >> 2) * 4096);
-          if (kFmt == MISA_KV_BF16 && row + (i >> 2) * 32 >= it.w.n) y[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();   // read before TMA may write there again
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) arrive_here(sb + kCopied + 8 * u);
-        if (turn == 0 && !wait_warp(sb + kVEmpty + 8 * rank, parity ^ 1u, p.a.err)) return;
-        if (u == rank) {
+      for (int b = 0; b < 8; ++b) y[b] = ld_shared16(src0 + n.stage() * kKStage + b * kKBlock);
+      if (tile * kTile + own >= it.w.n) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) st_shared16(dst + (i & 3) * kBlockBytes + (i >> 2) * 4096, y[i]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + 8 * rank, 0);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) st_async16(far + (i & 3) * kBlockBytes + (i >> 2) * 4096, y[i], far_bar);
-        }
+        for (int b = 0; b < 8; ++b) y[b] = make_uint4(0u, 0u, 0u, 0u);
       }
+      fence_proxy_async_smem();   // read before TMA may write there again
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) arrive_here(sb + kCopied + n.at());
+      if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return;
+      const uint32_t vofs = n.stage() * kVStage;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if ((b >> 2) == static_cast<int>(rank)) st_shared16(vdst0 + vofs + (b & 3) * kVBlock, y[b]);
+        else st_async16(far0 + vofs + (b & 3) * kVBlock, y[b], far_bar0 + n.at());
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + n.at(), 0);
     }
 }
-// Passes on to the first CTA what the other one has copied here, a warp.
-__device__ __forceinline__ void pass_copies(const MlaParams& p, uint32_t rank, int lane, uint32_t sb) {
-  uint32_t parity = 0;
-  if (lane == 0) bar_expect(sb + kVLanded, kVUnitBytes);
+
+// Passes on to the first CTA what the other one has written here, a warp.
+__device__ __forceinline__ void pass_values(const MlaParams& p, int lane, uint32_t sb) {
+  if (lane == 0) {
+    bar_expect(sb + kVLanded, kVStage / 2);
+    bar_expect(sb + kVLanded + 8, kVStage / 2);
+  }
+  Turn n;
   for (Items it(p); it.next(p);)
 #pragma unroll 1
-    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
-      if (!wait_warp(sb + kVLanded, parity, p.a.err)) return;
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
+      if (!wait_warp(sb + kVLanded + n.at(), n.parity(), p.a.err)) return;
       if (lane == 0) {
-        bar_expect(sb + kVLanded, kVUnitBytes);
+        bar_expect(sb + kVLanded + n.at(), kVStage / 2);   // for the tile after the next
         asm volatile("fence.proxy.async;" ::: "memory");
-        arrive_in(sb + kVFull + 8 * (rank ^ 1u), 0);
+        arrive_in(sb + kVFull + n.at(), 0);
       }
     }
 }
 
-// Brings the queries of this CTA's heads and asks the quantised rows of the tile
-// after the next into L2, a warp: in a prefix one request for the CTA's 64 rows,
-// else line by line.
+// Brings the queries of this CTA's heads, and asks the quantised rows of tiles ahead
+// into L2, a warp: in a prefix one request for the CTA's rows, else line by line.
+__device__ __forceinline__ void load_queries(const MlaParams& p, uint32_t rank, int t, const CUtensorMap* q_map, uint32_t sb) {
+  bar_expect(sb + kQFull, kBlocks * kQBlock);
+#pragma unroll 1
+  for (int b = 0; b < kBlocks; ++b)
+    tma_2d(sb + kOffQ + b * kQBlock, q_map, sb + kQFull, b * 64, t * p.a.Hq + static_cast<int>(rank) * kHeads);
+}
+constexpr int kAhead = 4;   // tiles
 template <int kFmt>
 __device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, int lane, const CUtensorMap* q_map, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
-  uint32_t parity = 1, items = 0;
+  uint32_t items = 0;
+  Turn n;
   for (Items it(p); it.next(p); ++items) {
     const Work& w = it.w;
     if (!wait_warp(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
-    if (elect_one()) {
-      bar_expect(sb + kQFull, kBlocks * kBlockBytes);
-#pragma unroll 1
-      for (int b = 0; b < kBlocks; ++b)
-        tma_2d(sb + kOffQ + b * kBlockBytes, q_map, sb + kQFull, b * 64, w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
-    }
+    if (elect_one()) load_queries(p, rank, w.t, q_map, sb);
     __syncwarp();
     if (!wait_warp(sb + kQFull, items & 1, p.a.err)) return;
     if (lane == 0) arrive_in(sb + kQReady, 0);
-    for (int tile = w.tile0; tile < w.tile1; ++tile, parity ^= 1u) {
+    for (int tile = w.tile0; tile < w.tile1; ++tile, ++n.n) {
       // Goes on with the tiles: S of this one waits for the arrival, so that no phase
       // can pass by unseen.
-      if (!wait_warp(sb + kKEmpty + 8, parity, p.a.err)) return;
-      if (lane == 0) arrive_in(sb + kKFull + 8, 0);
-      const int first = (tile + 2) * kTile + static_cast<int>(rank) * 64;
-      if (tile + 2 >= w.tile1) continue;
+      if (!wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return;
+      if (lane == 0) arrive_in(sb + kKFull + n.at(), 0);
+      if (tile + kAhead >= w.tile1) continue;
+      const int first = (tile + kAhead) * kTile + static_cast<int>(rank) * kRows;
       if (!w.idx) {
-        const int rows = min(64, w.n - first);
+        const int rows = min(kRows, w.n - first);
         if (lane == 0 && rows > 0)
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w.base + static_cast<int64_t>(first) * kRow), "r"(rows * kRow)
                        : "memory");
         continue;
       }
+      const int32_t id = row_of(w, first + lane);
+      if (id < 0) continue;
+      const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow;
 #pragma unroll 1
-      for (int r = lane; r < 64; r += 32) {
-        const int32_t id = row_of(w, first + r);
-        if (id < 0) continue;
-        const uint8_t* row = w.base + static_cast<int64_t>(id) * kRow;
-#pragma unroll 1
-        for (int o = 0; o < kRow; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + o));
-      }
+      for (int o = 0; o < kRow; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + o));
     }
   }
 }
 
 // Of a bf16 cache, brings queries and rows by TMA; one thread.
 __device__ __forceinline__ void ask_rows(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
-  uint32_t items = 0, parity = 1;
+  uint32_t items = 0;
+  Turn n;
   for (Items it(p); it.next(p); ++items) {
     if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
-    bar_expect(sb + kQFull, kBlocks * kBlockBytes);
-#pragma unroll 1
-    for (int b = 0; b < kBlocks; ++b)
-      tma_2d(sb + kOffQ + b * kBlockBytes, q_map, sb + kQFull, b * 64, it.w.t * p.a.Hq + static_cast<int>(rank) * kHeads);
-    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, parity ^= 1u) {
-      const int row = tile * kTile + static_cast<int>(rank) * 64;
+    load_queries(p, rank, it.w.t, q_map, sb);
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
+      const int row = tile * kTile + static_cast<int>(rank) * kRows;
+      const uint32_t bar = sb + kKHere + n.at();
+      if (!wait_one(sb + kKEmpty + n.at(), n.before(), p.a.err) || !wait_one(sb + kCopied + n.at(), n.before(), p.a.err)) return;
+      bar_expect(bar, kKStage);
 #pragma unroll 1
       for (int b = 0; b < kBlocks; ++b) {
-        const uint32_t u = b >= 4;
-        if ((b & 3) == 0 && b < 8) {
-          if (!wait_one(sb + kKEmpty + 8 * u, parity, p.a.err) || !wait_one(sb + kCopied + 8 * u, parity, p.a.err)) return;
-          bar_expect(sb + kKHere + 8 * u, (u ? 5 : 4) * kBlockBytes);
-        }
-        tma_3d(sb + kOffK + b * kBlockBytes, map, sb + kKHere + 8 * u, b * 64, row, it.w.seq);
-        if (tile + 2 < it.w.tile1) tma_l2_3d(map, b * 64, row + 2 * kTile, it.w.seq);   // two tiles ahead into L2
+        tma_3d(sb + kOffK + n.stage() * kKStage + b * kKBlock, map, bar, b * 64, row, it.w.seq);
+        if (tile + kAhead < it.w.tile1) tma_l2_3d(map, b * 64, row + kAhead * kTile, it.w.seq);
       }
     }
   }
 }
 // Passes on to the first CTA what has landed, one thread.
 __device__ __forceinline__ void pass_rows(const MlaParams& p, uint32_t sb) {
-  uint32_t items = 0, parity = 0;
+  uint32_t items = 0;
+  Turn n;
   for (Items it(p); it.next(p); ++items) {
     if (!wait_one(sb + kQFull, items & 1, p.a.err)) return;
     arrive_in(sb + kQReady, 0);
 #pragma unroll 1
-    for (int unit = it.w.tile0 * kUnits; unit < it.w.tile1 * kUnits; ++unit) {
-      const uint32_t u = unit & 1;
-      if (!wait_one(sb + kKHere + 8 * u, parity, p.a.err)) return;
-      arrive_in(sb + kKFull + 8 * u, 0);
-      parity ^= u;
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
+      if (!wait_one(sb + kKHere + n.at(), n.parity(), p.a.err)) return;
+      arrive_in(sb + kKFull + n.at(), 0);
     }
   }
 }
 
 // Issues the products of both CTAs, a warp of the first.  Two rows of work over the
-// items, S of one tile after the other and O += P V; whatever has its operands next
+// items, S of one tile after the other and O += P V; whichever has its operands next
 // is issued, O first.  The warp looks at all the barriers together, and one lane
-// issues a unit.
+// issues a tile's.
 __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint32_t sb) {
   const bool leader = elect_one();
   Items si(p), oi(p);
   int s_left = 0, o_left = 0;           // tiles of the item at hand
   bool s_any = true, s_first = false, o_first = false;
-  uint32_t st = 0, ot = 0;              // tiles so far
-  uint32_t s_unit = 0, o_unit = 0;
+  Turn s, o;
   uint32_t s_items = 0, o_items = 0;    // items begun
   uint32_t t0 = clock();
   while (true) {
@@ -596,69 +592,67 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
       o_first = true;
       ++o_items;
     }
-    uint32_t ready = test_phase(sb + kPFull, ot & 1);
-    ready |= test_phase(sb + kVFull + 8 * o_unit, ot & 1) << 1;
+    uint32_t ready = test_phase(sb + kPFull + o.at(), o.parity());
+    ready |= test_phase(sb + kVFull + o.at(), o.parity()) << 1;
     ready |= test_phase(sb + kOEmpty, o_items & 1) << 2;               // the item before's (o_items - 2)
-    ready |= test_phase(sb + kSEmpty + 8 * (st & 1), ((st >> 1) & 1) ^ 1u) << 3;
-    ready |= test_phase(sb + kKFull + 8 * s_unit, st & 1) << 4;
+    ready |= test_phase(sb + kSEmpty + s.at(), s.before()) << 3;
+    ready |= test_phase(sb + kKFull + s.at(), s.parity()) << 4;
     ready |= test_phase(sb + kQReady, (s_items - 1) & 1) << 5;
     ready = __reduce_and_sync(0xffffffffu, ready);
-    if (o_unit) ready |= 1u;                       // looked at with the tile's first unit
-    if (o_unit || !o_first || o_items == 1) ready |= 4u;
-    if (s_unit) ready |= 8u;
-    if (s_unit || !s_first) ready |= 32u;
-    if (ot < st && (ready & 7u) == 7u) {
+    if (!o_first || o_items == 1) ready |= 4u;
+    if (!s_first) ready |= 32u;
+    if (o.n < s.n && (ready & 7u) == 7u) {
       if (leader) {
         tc_fence_after();
-        const uint64_t w = sw128_kmajor_desc(sb + kOffP + o_unit * kBlockBytes);
-        const uint64_t v = sw128_mnmajor_desc(sb + kOffV + o_unit * kVUnitBytes, kBlockBytes);
-        const uint32_t add = o_unit || !o_first;
+        const uint64_t w = sw128_kmajor_desc(sb + kOffP + o.stage() * kPStage);
+        const uint64_t v = sw128_mnmajor_desc(sb + kOffV + o.stage() * kVStage, kVBlock);
+        const uint32_t add = !o_first;
         umma_pair<0, 0>(tmem, w, v, kIdescO, add);                      // 16 rows, entries 0 .. 127 of each half
-        umma_pair<0, 2 * kBlockBytes>(tmem + 128, w, v, kIdescO, add);
+        umma_pair<0, 2 * kVBlock>(tmem + 128, w, v, kIdescO, add);
         umma_pair<32, 2048>(tmem, w, v, kIdescO, 1);
-        umma_pair<32, 2 * kBlockBytes + 2048>(tmem + 128, w, v, kIdescO, 1);
+        umma_pair<32, 2 * kVBlock + 2048>(tmem + 128, w, v, kIdescO, 1);
         umma_pair<64, 4096>(tmem, w, v, kIdescO, 1);
-        umma_pair<64, 2 * kBlockBytes + 4096>(tmem + 128, w, v, kIdescO, 1);
+        umma_pair<64, 2 * kVBlock + 4096>(tmem + 128, w, v, kIdescO, 1);
         umma_pair<96, 6144>(tmem, w, v, kIdescO, 1);
-        umma_pair<96, 2 * kBlockBytes + 6144>(tmem + 128, w, v, kIdescO, 1);
-        commit_pair(sb + kVEmpty + 8 * o_unit);
-        if (o_unit) commit_pair(sb + kPvDone);
+        umma_pair<96, 2 * kVBlock + 6144>(tmem + 128, w, v, kIdescO, 1);
+        commit_pair(sb + kVEmpty + o.at());
+        commit_pair(sb + kPvDone + o.at());
       }
-      if (o_unit) {
-        ++ot;
-        --o_left;
-        o_first = false;
-      }
-      o_unit ^= 1u;
+      ++o.n;
+      --o_left;
+      o_first = false;
       t0 = clock();
-    } else if (s_left && st < ot + 2 && (ready & 56u) == 56u) {
+    } else if (s_left && s.n < o.n + 2 && (ready & 56u) == 56u) {
       if (leader) {
         tc_fence_after();
-        const uint32_t d = tmem + kTmemS + (st & 1) * 64;
-        uint64_t q = sw128_kmajor_desc(sb + kOffQ + s_unit * kKUnitBytes), k = sw128_kmajor_desc(sb + kOffK + s_unit * kKUnitBytes);
-        uint32_t add = s_unit;
+        const uint32_t d = tmem + kTmemS + s.stage() * 32;
+        uint64_t q = sw128_kmajor_desc(sb + kOffQ), k = sw128_kmajor_desc(sb + kOffK + s.stage() * kKStage);
+        uint32_t add = 0;
 #pragma unroll 1
-        for (uint32_t b = 0; b < 4 + s_unit; ++b) {
+        for (int b = 0; b < kBlocks; b += 3) {
           umma_pair<0, 0>(d, q, k, kIdescS, add);
           umma_pair<32, 32>(d, q, k, kIdescS, 1);
           umma_pair<64, 64>(d, q, k, kIdescS, 1);
           umma_pair<96, 96>(d, q, k, kIdescS, 1);
+          umma_pair<kQBlock, kKBlock>(d, q, k, kIdescS, 1);
+          umma_pair<kQBlock + 32, kKBlock + 32>(d, q, k, kIdescS, 1);
+          umma_pair<kQBlock + 64, kKBlock + 64>(d, q, k, kIdescS, 1);
+          umma_pair<kQBlock + 96, kKBlock + 96>(d, q, k, kIdescS, 1);
+          umma_pair<2 * kQBlock, 2 * kKBlock>(d, q, k, kIdescS, 1);
+          umma_pair<2 * kQBlock + 32, 2 * kKBlock + 32>(d, q, k, kIdescS, 1);
+          umma_pair<2 * kQBlock + 64, 2 * kKBlock + 64>(d, q, k, kIdescS, 1);
+          umma_pair<2 * kQBlock + 96, 2 * kKBlock + 96>(d, q, k, kIdescS, 1);
           add = 1;
-          q += kBlockBytes >> 4;
-          k += kBlockBytes >> 4;
+          q += 3 * kQBlock >> 4;
+          k += 3 * kKBlock >> 4;
         }
-        commit_pair(sb + kKEmpty + 8 * s_unit);
-        if (s_unit) {
-          commit_pair(sb + kSFull + 8 * (st & 1));
-          if (s_left == 1) commit_pair(sb + kQEmpty);
-        }
+        commit_pair(sb + kKEmpty + s.at());
+        commit_pair(sb + kSFull + s.at());
+        if (s_left == 1) commit_pair(sb + kQEmpty);
       }
-      if (s_unit) {
-        ++st;
-        --s_left;
-        s_first = false;
-      }
-      s_unit ^= 1u;
+      ++s.n;
+      --s_left;
+      s_first = false;
       t0 = clock();
     } else if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) {
       record_error(p.a.err, MISA_DEVERR_TIMEOUT);
@@ -671,31 +665,31 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(block_threads(kFmt), 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap row_map, const MlaParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  constexpr int kMmaWarp = first_copy_warp(kFmt) + kCopyWarps;
+  constexpr bool kQuant = kFmt != MISA_KV_BF16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   if (tid == 0) {
-    constexpr uint32_t kWriters = kFmt == MISA_KV_BF16 ? 1 : kRowWarps;   // that arrive in a CTA
-    for (int i = 0; i < kUnits; ++i) {
-      bar_init(sb + kKFull + 8 * i, 2 * kWriters + (i && kFmt != MISA_KV_BF16 ? 2 : 0));   // and look_ahead
-      bar_init(sb + kKHere + 8 * i, kWriters);
-      bar_init(sb + kKEmpty + 8 * i, 1);
-      bar_init(sb + kCopied + 8 * i, kCopyWarps);
-      bar_init(sb + kVFull + 8 * i, kCopyWarps + 1);   // of the CTA whose rows they are, and pass_copies of the other
-      bar_init(sb + kVEmpty + 8 * i, 1);
+    for (uint32_t at = 0; at < 16; at += 8) {
+      bar_init(sb + kKFull + at, kQuant ? 2 * (kRowWarps + 1) : 2);   // bring_rows and look_ahead, or pass_rows
+      bar_init(sb + kKHere + at, 1);
+      bar_init(sb + kKEmpty + at, 1);
+      bar_init(sb + kCopied + at, kRowWarps);
+      bar_init(sb + kVFull + at, 2 * (kRowWarps + 1));                // and pass_values
+      bar_init(sb + kVLanded + at, 1);
+      bar_init(sb + kVEmpty + at, 1);
+      bar_init(sb + kSFull + at, 1);
+      bar_init(sb + kSEmpty + at, 8);
+      bar_init(sb + kPFull + at, 8);
+      bar_init(sb + kPvDone + at, 1);
     }
-    bar_init(sb + kVLanded, 1);
-    for (int i = 0; i < 2; ++i) { bar_init(sb + kSFull + 8 * i, 1); bar_init(sb + kSEmpty + 8 * i, 8); }
-    bar_init(sb + kPFull, 8);
-    bar_init(sb + kPvDone, 1);
     bar_init(sb + kOEmpty, 8);
-    bar_init(sb + kQEmpty, 1);
     bar_init(sb + kQFull, 1);
     bar_init(sb + kQReady, 2);
+    bar_init(sb + kQEmpty, 1);
     bar_init(sb + kDone, 1);
     fence_mbar_init();
   }
@@ -717,49 +711,37 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 
   const LatentArgs& a = p.a;
   uint32_t* err = a.err;
-  // Registers of the warpgroups: 152 + 2 * 64 + 2 * 64 + 72 of 6 * 80, or 168 + 2 * 112 + 120 of 4 * 128
-  constexpr bool kQuant = kFmt != MISA_KV_BF16;
-  if (warp >= kMmaWarp) {
-    if (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    if (warp == kMmaWarp) {
-      if (rank == 0) multiply(p, tmem, sb);
-      wait_all(sb, err);   // nothing reads this CTA's memory any more
+  if (warp == kMmaWarp) {
+    if (rank == 0) multiply(p, tmem, sb);
+    wait_all(sb, err);   // nothing reads this CTA's memory any more
+    __syncwarp();
+  } else if (warp == kMmaWarp + 1) {
+    pass_values(p, lane, sb);
+  } else if (warp == kMmaWarp + 2) {
+    if constexpr (kQuant) {
+      look_ahead<kFmt>(p, rank, lane, &q_map, sb);
+    } else {
+      if (elect_one()) ask_rows(p, rank, &q_map, &row_map, sb);
       __syncwarp();
-    } else if (warp == kMmaWarp + 1) {
-      if constexpr (kQuant) {
-        look_ahead<kFmt>(p, rank, lane, &q_map, sb);
-      } else {
-        if (elect_one()) ask_rows(p, rank, &q_map, &row_map, sb);
-        __syncwarp();
-      }
-    } else if (warp == kMmaWarp + 2) {
-      pass_copies(p, rank, lane, sb);
-    } else if constexpr (!kQuant) {
+    }
+  } else if (warp == kMmaWarp + 3) {
+    if constexpr (!kQuant) {
       if (elect_one()) pass_rows(p, sb);
       __syncwarp();
     }
-  } else if (warp >= first_copy_warp(kFmt)) {
-    if (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    copy_rows<kFmt>(p, rank, tid - first_copy_warp(kFmt) * 32, sb);
   } else if (warp >= 4) {
-    if constexpr (kQuant) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-      bring_rows<kFmt>(p, rank, tid - 128, sb);
-    }
+    if constexpr (kQuant) bring_rows<kFmt>(p, rank, tid - 128, sb);
+    else copy_rows(p, rank, tid - 128, sb);
   } else {
-    if (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // ------------------------------------------------------------ softmax and output
-    const int half = warp >> 1;                     // rows [64 half, 64 half + 64) of a tile, entries 256 half .. of O
+    const int half = warp >> 1;                     // rows [32 half, 32 half + 32) of a tile, entries 256 half .. of O
     const int hl = (warp & 1) * 32 + lane;          // head of this CTA
     const int h = static_cast<int>(rank) * kHeads + hl;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const float kNegInf = -__int_as_float(0x7f800000);
     const float c = fmaxf(a.scale_log2, 1.2e-38f);   // a scale of 0 weighs all rows alike; -inf stays -inf
     bool ok = true;
-    uint32_t st = 0;    // tiles so far
+    Turn n;
     Peek ahead = peek(p, static_cast<int>(blockIdx.x >> 1));
     for (int item = static_cast<int>(blockIdx.x >> 1); item < p.items; item += static_cast<int>(gridDim.x >> 1)) {
     const Work w = work_of(p, item, ahead);
@@ -767,34 +749,31 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     ahead = peek(p, item + static_cast<int>(gridDim.x >> 1));
     const int ntiles = w.tile1 - w.tile0;
     float m = kNegInf, l = 0.f;
-    for (int i = 0; i < ntiles; ++i, ++st) {
-      // rows of this half that exist: two words, the same in the whole warp
-      uint32_t live[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        live[j] = __ballot_sync(0xffffffffu, row_of(w, (w.tile0 + i) * kTile + half * 64 + j * 32 + lane) >= 0);
+    int32_t here = ntiles > 0 ? row_of(w, w.tile0 * kTile + half * 32 + lane) : -1;   // this lane's row of the half
+    for (int i = 0; i < ntiles; ++i, ++n.n) {
+      const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);   // rows of this half that exist
       // a wait that gave up ends the work, not the loop: the warps' barriers stay paired
-      ok = ok && wait_warp(sb + kSFull + 8 * (st & 1), (st >> 1) & 1, err);
-      uint32_t s[64];
+      ok = ok && wait_warp(sb + kSFull + n.at(), n.parity(), err);
+      uint32_t s[32];
       float mx = kNegInf;
       if (ok) {
         tc_fence_after();
-        tmem_ld32(t_lane + kTmemS + (st & 1) * 64, s);
-        tmem_ld32(t_lane + kTmemS + (st & 1) * 64 + 32, s + 32);
+        tmem_ld32(t_lane + kTmemS + n.stage() * 32, s);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_in(sb + kSEmpty + 8 * (st & 1), 0);
-        if ((live[0] & live[1]) != 0xffffffffu) {
+        if (lane == 0) arrive_in(sb + kSEmpty + n.at(), 0);
+        if (live != 0xffffffffu) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (!((live[j >> 5] >> (j & 31)) & 1u)) s[j] = 0xff800000u;
+          for (int j = 0; j < 32; ++j)
+            if (!((live >> j) & 1u)) s[j] = 0xff800000u;
         }
 #pragma unroll
-        for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
+        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
       }
+      if (i + 1 < ntiles) here = row_of(w, (w.tile0 + i + 1) * kTile + half * 32 + lane);
       // the other half of the tile's rows for the same head
-      const uint32_t red = sb + kOffRed + (st & 1) * 512;
+      const uint32_t red = sb + kOffRed + n.stage() * 512;
       st_shared(red + tid * 4, __float_as_uint(mx));
       named_bar_sync(1, 128);
       mx = fmaxf(mx, __uint_as_float(ld_shared(red + (tid ^ 64) * 4))) * c;
@@ -807,45 +786,48 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       const float mr = m == kNegInf ? 0.f : m;
       float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {   // (the packed pairs take the place of the scores)
+      for (int j = 0; j < 32; j += 2) {   // (the packed pairs take the place of the scores)
         const float x = ex2(fmaf(__uint_as_float(s[j]), c, -mr)), y = ex2(fmaf(__uint_as_float(s[j + 1]), c, -mr));
         l0 += x;
         l1 += y;
         s[j >> 1] = pack_bf16(x, y);
       }
       l += l0 + l1;
-      if (i > 0) ok = ok && wait_warp(sb + kPvDone, (st - 1) & 1, err);
-      if (!ok) continue;
-      if (i > 0) {
+      // P's stage is free once O of two tiles ago is done; O is scaled once the last one is
+      ok = ok && wait_warp(sb + kPvDone + n.at(), n.before(), err);
+      if (__any_sync(0xffffffffu, f != 1.f) && i > 0 && ok) {
+        Turn last = n;
+        --last.n;
+        ok = wait_warp(sb + kPvDone + last.at(), last.parity(), err);
         tc_fence_after();
-        if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-          for (int o = 0; o < 256; o += 32) {
-            uint32_t v[32];
-            tmem_ld32(t_lane + o, v);
-            tmem_wait_ld();
+        for (int o = 0; o < 256; o += 16) {
+          uint32_t v[16];
+          tmem_ld16(t_lane + o, v);
+          tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-            tmem_st16(t_lane + o, v);
-            tmem_st16(t_lane + o + 16, v + 16);
-          }
-          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+          tmem_st16(t_lane + o, v);
         }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
       }
-      const uint32_t prow = sb + kOffP + half * kBlockBytes + hl * 128;
+      if (!ok) continue;
+      const uint32_t prow = sb + kOffP + n.stage() * kPStage + hl * 128;
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        st_shared16(prow + ((u ^ (hl & 7)) << 4), make_uint4(s[4 * u], s[4 * u + 1], s[4 * u + 2], s[4 * u + 3]));
-      tc_fence_before();
+      for (int u = 0; u < 4; ++u)
+        st_shared16(prow + (((half * 4 + u) ^ (hl & 7)) << 4), make_uint4(s[4 * u], s[4 * u + 1], s[4 * u + 2], s[4 * u + 3]));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_in(sb + kPFull, 0);
+      if (lane == 0) arrive_in(sb + kPFull + n.at(), 0);
     }
+    Turn last = n;
+    --last.n;
     if (ntiles > 0) {   // both halves' sums
       st_shared(sb + kOffRed + 1024 + tid * 4, __float_as_uint(l));
       named_bar_sync(1, 128);
       l += __uint_as_float(ld_shared(sb + kOffRed + 1024 + (tid ^ 64) * 4));
-      ok = ok && wait_warp(sb + kPvDone, (st - 1) & 1, err);
+      ok = ok && wait_warp(sb + kPvDone + last.at(), last.parity(), err);
       tc_fence_after();
     }
     // Output by 128 bytes a row: each warp turns its 32 heads' pieces round in its
@@ -970,9 +952,9 @@ latent_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
 // Clusters that run at once on the 148 SMs of a B200.
 constexpr int kSlots = 74;
 
-// How many items share a query's rows.  An item takes its tiles and about one and
-// a half tiles' worth of queries and output, a join about three more at the end;
-// the split that makes the busiest cluster's list shortest is taken.
+// How many items share a query's rows.  An item takes its tiles and about five
+// tiles' worth of queries and output, a join about four more at the end; the split
+// that makes the busiest cluster's list shortest is taken.
 int pick_splits(int T, int64_t n) {
   const int64_t tiles = (n + kTile - 1) / kTile;
   int best = 1;
@@ -980,7 +962,7 @@ int pick_splits(int T, int64_t n) {
   for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
     if (s > 1 && static_cast<int64_t>(T) * s > 4 * kSlots) break;
     const int64_t rounds = (static_cast<int64_t>(T) * s + kSlots - 1) / kSlots;
-    const int64_t cost = rounds * (2 * ((tiles + s - 1) / s) + 3) + (s > 1 ? 6 : 0);
+    const int64_t cost = rounds * ((tiles + s - 1) / s + 5) + (s > 1 ? 4 : 0);
     if (best_cost < 0 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -1008,7 +990,7 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   CUtensorMap rmap = qmap;   // (quantised rows go by plain loads)
   if (a.fmt == MISA_KV_BF16 &&
       !encode_3d_map(&rmap, a.cache, kDqk, static_cast<uint64_t>(a.L), static_cast<uint64_t>(a.nseq), kDqk * 2,
-                     a.nseq > 1 ? static_cast<uint64_t>(a.seq_stride) : static_cast<uint64_t>(a.L) * kDqk * 2, 64, 64))
+                     a.nseq > 1 ? static_cast<uint64_t>(a.seq_stride) : static_cast<uint64_t>(a.L) * kDqk * 2, 64, kRows))
     return cudaErrorInvalidValue;
   auto kern = a.fmt == MISA_KV_BF16  ? latent_mla_kernel<MISA_KV_BF16>
               : a.fmt == MISA_KV_MX8 ? latent_mla_kernel<MISA_KV_MX8>
@@ -1018,7 +1000,7 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   p.items = a.T * p.nsplit;
   p.by_nsplit = p.nsplit > 1 ? static_cast<uint32_t>(((1ull << 32) + p.nsplit - 1) / p.nsplit) : 0u;
   const int clusters = p.items < kSlots ? p.items : kSlots;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(block_threads(a.fmt)), kSmemBytes, stream, 0, qmap, rmap, p);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * a.Hq), dim3(128), 0, stream, 0,
                     static_cast<const float*>(p.part_o), static_cast<const float*>(p.part_ml), a.Hq, p.nsplit, a.out, a.lse);
