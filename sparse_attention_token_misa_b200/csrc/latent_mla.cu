@@ -39,15 +39,13 @@
 // around 3 us a tile.)  Few queries: the rows of each are split over several
 // items, whose partial sums a second kernel joins in a fixed order.
 //
-// Roles, by warpgroups: warps 0-3 softmax and output (a lane of TMEM each); 8 warps
-// that bring quantised rows (none for bf16); 8 that copy; then one warp that has TMEM
-// and, in the first CTA, issues the MMAs, and one or two that ask for what comes by
-// TMA and pass on what has landed.  The softmax holds a tile's 64 scores a lane and
-// more, so the other warpgroups give it registers.  Shared memory is addressed from
-// one 32-bit base: with a pointer a barrier the kernel spilled, and what shared
-// memory leaves of L1 does not hold the stack.  Code is kept small (loops, not
-// copies): at 140 KB the instruction caches, which many SMs share, halved the speed.
-// Waits are bounded.
+// Roles (640 threads a CTA): two warpgroups softmax and output, eight warps that bring
+// quantised rows or copy bf16 ones, one warp that has TMEM and, in the first CTA,
+// issues the MMAs, and three that ask for what comes by TMA and pass on what has
+// landed.  Shared memory is addressed from one 32-bit base: with a pointer a barrier
+// the kernel spilled, and what shared memory leaves of L1 does not hold the stack.
+// Code is kept small (loops, not copies): at 140 KB the instruction caches, which
+// many SMs share, halved the speed.  Waits are bounded.
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"
@@ -89,11 +87,13 @@ constexpr uint32_t kQReady = kQFull + 8;          // (one) first CTA: both CTAs'
 constexpr uint32_t kQEmpty = kQReady + 8;         // (one) the item's last S complete
 constexpr uint32_t kDone = kQEmpty + 8;           // (one) every MMA retired
 constexpr uint32_t kOffTmem = kDone + 8;
-constexpr uint32_t kOffRed = (kOffTmem + 8 + 15) / 16 * 16;   // [3][128] floats
-constexpr int kSmemBytes = kOffRed + 3 * 128 * 4 + 1024;
+constexpr uint32_t kOffMax = (kOffTmem + 8 + 15) / 16 * 16;   // [2][128] floats: a tile's maxima, by softmax warpgroup
+constexpr uint32_t kOffRef = kOffMax + 1024;      // [2][64]: a head's reference m after a tile
+constexpr uint32_t kOffSum = kOffRef + 512;       // [2][128]: an item's sums of the warpgroup that does not finish it
+constexpr int kSmemBytes = kOffSum + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-// Warps: 0-3 softmax and output, 4-11 bring quantised rows or copy bf16 ones, 12-15 the rest.
-constexpr int kRowWarps = 8, kMmaWarp = 4 + kRowWarps, kThreads = (kMmaWarp + 4) * 32;
+// Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-19 the rest.
+constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps, kThreads = (kMmaWarp + 4) * 32;
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 32 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 64);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -664,11 +664,220 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
   __syncwarp();
 }
 
+// Named barriers: the maxima of a tile (128 threads, by warpgroup), the reference
+// after a tile (256, by the tile's number), an item's sums (256, by the item's).
+constexpr int kBarMax = 1, kBarRef = 3, kBarSum = 5;
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// Softmax and output, two warpgroups: each takes every other tile, so that one's
+// loads, barriers and fences pass while the other one counts; between them goes the
+// reference m alone, early in a tile.  tid: in the warpgroup; its warp w has TMEM
+// lanes 32 w.., two lanes a head, one for each half of a tile's rows and of O.
+__device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint32_t group, int tid, uint32_t tmem, uint32_t sb) {
+  const LatentArgs& a = p.a;
+  uint32_t* err = a.err;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int half = warp >> 1;                     // rows [32 half, 32 half + 32) of a tile, entries 256 half .. of O
+  const int hl = (warp & 1) * 32 + lane;          // head of this CTA
+  const int h = static_cast<int>(rank) * kHeads + hl;
+  const int h0 = static_cast<int>(rank) * kHeads + (warp & 1) * 32;   // first head of the warp
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const float kNegInf = -__int_as_float(0x7f800000);
+  const float c = fmaxf(a.scale_log2, 1.2e-38f);   // a scale of 0 weighs all rows alike; -inf stays -inf
+  const uint32_t my_p = sb + kOffP + group * kPStage;
+  bool ok = true;
+  Turn n;
+  uint32_t items = 0;                              // that have rows, so far
+  const int step = static_cast<int>(gridDim.x >> 1);
+  Peek ahead = peek(p, static_cast<int>(blockIdx.x >> 1));
+  for (int item = static_cast<int>(blockIdx.x >> 1); item < p.items; item += step) {
+    const Work w = work_of(p, item, ahead);
+    if (tid == 0 && group == 0 && rank == 0 && (ahead.seq < 0 || ahead.seq >= a.nseq)) record_error(err, MISA_DEVERR_BAD_SEQ);
+    ahead = peek(p, item + step);
+    const int ntiles = w.tile1 - w.tile0;
+    const int64_t row0 = (p.nsplit > 1 ? static_cast<int64_t>(w.t) * p.nsplit + w.split : static_cast<int64_t>(w.t)) * a.Hq;
+    if (ntiles == 0) {   // no rows: zeros, and a sum of nothing
+      if (group == 0) {
+        if (h < a.Hq && half == 0) {
+          if (p.nsplit > 1) *reinterpret_cast<float2*>(p.part_ml + (row0 + h) * 2) = make_float2(kNegInf, 0.f);
+          else if (a.lse) a.lse[row0 + h] = kNegInf;
+        }
+        for (int x = tid; p.nsplit == 1 && x < kHeads * 64; x += 128)
+          if (static_cast<int>(rank) * kHeads + (x >> 6) < a.Hq)
+            reinterpret_cast<uint4*>(a.out + (row0 + rank * kHeads) * kDv)[x] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
+    }
+    const uint32_t first = n.n, end = n.n + ntiles;
+    n.n += (n.n ^ group) & 1;                      // the first tile of this warpgroup
+    float m_prev = kNegInf, m = kNegInf, l = 0.f;  // m: the reference that l is relative to
+    auto row_at = [&](uint32_t t) {                // this lane's row of the half of tile number t
+      return t < end ? row_of(w, (w.tile0 + static_cast<int>(t - first)) * kTile + half * 32 + lane) : -1;
+    };
+    int32_t here = row_at(n.n);
+#pragma unroll 1
+    for (; n.n < end; n.n += 2) {
+      const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);   // rows of this half that exist
+      // A wait that gave up ends the work, not the loop: the barriers stay paired.  S
+      // complete also says that O of two tiles ago is, which read this place of P.
+      ok = ok && wait_warp(sb + kSFull + n.at(), n.parity(), err);
+      uint32_t s[32];
+      float mx = kNegInf;
+      if (ok) {
+        tc_fence_after();
+        tmem_ld32(t_lane + kTmemS + group * 32, s);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_in(sb + kSEmpty + n.at(), 0);
+        if (live != 0xffffffffu) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!((live >> j) & 1u)) s[j] = 0xff800000u;
+        }
+        float x[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j & 3] = fmaxf(x[j & 3], __uint_as_float(s[j]));
+        mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      }
+      here = row_at(n.n + 2);
+      // the other half of the tile's rows for the same head
+      st_shared(sb + kOffMax + group * 512 + tid * 4, __float_as_uint(mx));
+      named_bar_sync(kBarMax + group, 128);
+      mx = fmaxf(mx, __uint_as_float(ld_shared(sb + kOffMax + group * 512 + (tid ^ 64) * 4))) * c;
+      // the reference after the tile before, moved if this tile is far above it
+      m_prev = kNegInf;
+      if (n.n > 0) {
+        named_bar_sync(kBarRef + (group ^ 1u), 256);
+        if (n.n > first) m_prev = __uint_as_float(ld_shared(sb + kOffRef + (group ^ 1u) * 256 + hl * 4));
+      }
+      const bool moved = mx > m_prev + 8.f || (m_prev == kNegInf && mx > kNegInf);
+      const float m_new = moved ? mx : m_prev;
+      if (half == 0) st_shared(sb + kOffRef + group * 256 + hl * 4, __float_as_uint(m_new));
+      named_bar_arrive(kBarRef + group, 256);
+      if (m_new != m) {
+        l *= m == kNegInf ? 0.f : ex2(m - m_new);
+        m = m_new;
+      }
+      const float mr = m == kNegInf ? 0.f : m;
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {   // (the packed pairs take the place of the scores)
+        const float x = ex2(fmaf(__uint_as_float(s[j]), c, -mr)), y = ex2(fmaf(__uint_as_float(s[j + 1]), c, -mr));
+        l0 += x;
+        l1 += y;
+        s[j >> 1] = pack_bf16(x, y);
+      }
+      l += l0 + l1;
+      if (!ok) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        st_shared16(my_p + hl * 128 + (((half * 4 + u) ^ (hl & 7)) << 4), make_uint4(s[4 * u], s[4 * u + 1], s[4 * u + 2], s[4 * u + 3]));
+      if (n.n > first && __any_sync(0xffffffffu, moved)) {   // O so far, once it is complete
+        Turn last = n;
+        --last.n;
+        ok = wait_warp(sb + kPvDone + last.at(), last.parity(), err);
+        const float f = !moved ? 1.f : m_prev == kNegInf ? 0.f : ex2(m_prev - m_new);
+        tc_fence_after();
+#pragma unroll 1
+        for (int o = 0; o < 256; o += 16) {
+          uint32_t v[16];
+          tmem_ld16(t_lane + o, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+          tmem_st16(t_lane + o, v);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_in(sb + kPFull + n.at(), 0);
+    }
+    n.n = end;
+    const uint32_t turn = items & 1;
+    ++items;
+    if (((end - 1) & 1) != group) {   // the other warpgroup finishes the item
+      st_shared(sb + kOffSum + turn * 512 + tid * 4, __float_as_uint(l));
+      named_bar_arrive(kBarSum + turn, 256);
+      continue;
+    }
+    // The sums of both warpgroups and both halves: the other warpgroup's are relative
+    // to the reference before the last tile.
+    named_bar_sync(kBarMax + group, 128);   // the last tile's maxima have been read
+    st_shared(sb + kOffMax + group * 512 + tid * 4, __float_as_uint(l));
+    named_bar_sync(kBarSum + turn, 256);
+    l += __uint_as_float(ld_shared(sb + kOffMax + group * 512 + (tid ^ 64) * 4));
+    named_bar_sync(kBarMax + group, 128);   // and so have these
+    if (ntiles > 1) {
+      const float other = __uint_as_float(ld_shared(sb + kOffSum + turn * 512 + tid * 4)) +
+                          __uint_as_float(ld_shared(sb + kOffSum + turn * 512 + (tid ^ 64) * 4));
+      l += other * (m_prev == m ? 1.f : m_prev == kNegInf ? 0.f : ex2(m_prev - m));
+    }
+    Turn last;
+    last.n = end - 1;
+    ok = ok && wait_warp(sb + kPvDone + last.at(), last.parity(), err);
+    tc_fence_after();
+    // Output: each warp turns its 32 heads' pieces round in its 2 KB of this
+    // warpgroup's place of P, so that four lanes store 64 bytes of a row.  (Stored
+    // straight from TMEM's lanes, each to a row of its own, an item's output took 4 us.)
+    const bool any = l > 0.f || l != l;
+    if (h < a.Hq && half == 0) {
+      if (p.nsplit > 1) *reinterpret_cast<float2*>(p.part_ml + (row0 + h) * 2) = make_float2(any ? m : kNegInf, l);
+      else if (a.lse) a.lse[row0 + h] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+    }
+    const uint32_t turn_p = my_p + warp * 2048;
+    const bool part = p.nsplit > 1;
+    const float inv = part ? 1.f : any ? 1.f / l : 0.f;
+    const int64_t row_bytes = part ? kDv * 4 : kDv * 2;
+    uint8_t* out = (part ? reinterpret_cast<uint8_t*>(p.part_o) : reinterpret_cast<uint8_t*>(a.out)) + (row0 + h0) * row_bytes +
+                   half * (row_bytes / 2) + (lane & 3) * 16;
+    const int rows = ok ? min(32, a.Hq - h0) : 0;
+#pragma unroll 1
+    for (int o = 0; o < 256; o += 16) {
+      uint32_t v[16];
+      tmem_ld16(t_lane + o, v);
+      tmem_wait_ld();
+      // 16 entries a lane: 64 bytes as they are, or with the next 16 as bf16
+      const uint32_t at = turn_p + lane * 64, swz = (lane >> 1) & 3;
+      if (part) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st_shared16(at + ((j ^ swz) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            x[u] = pack_bf16(__uint_as_float(v[8 * j + 2 * u]) * inv, __uint_as_float(v[8 * j + 2 * u + 1]) * inv);
+          st_shared16(at + ((((o >> 3) & 2) + j) ^ swz) * 16, make_uint4(x[0], x[1], x[2], x[3]));
+        }
+        if (!(o & 16)) continue;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = j * 8 + (lane >> 2);
+        if (r < rows) *reinterpret_cast<uint4*>(out + r * row_bytes) = ld_shared16(turn_p + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+      }
+      out += 64;
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_in(sb + kOEmpty, 0);   // O has been read
+  }
+}
+
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap row_map, const MlaParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];   // swizzled operands
+  const uint32_t sb = smem_u32(smem_raw);
   constexpr bool kQuant = kFmt != MISA_KV_BF16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -729,176 +938,11 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       if (elect_one()) pass_rows(p, sb);
       __syncwarp();
     }
-  } else if (warp >= 4) {
-    if constexpr (kQuant) bring_rows<kFmt>(p, rank, tid - 128, sb);
-    else copy_rows(p, rank, tid - 128, sb);
+  } else if (warp >= kRowWarp0) {
+    if constexpr (kQuant) bring_rows<kFmt>(p, rank, tid - kRowWarp0 * 32, sb);
+    else copy_rows(p, rank, tid - kRowWarp0 * 32, sb);
   } else {
-    // ------------------------------------------------------------ softmax and output
-    const int half = warp >> 1;                     // rows [32 half, 32 half + 32) of a tile, entries 256 half .. of O
-    const int hl = (warp & 1) * 32 + lane;          // head of this CTA
-    const int h = static_cast<int>(rank) * kHeads + hl;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const float kNegInf = -__int_as_float(0x7f800000);
-    const float c = fmaxf(a.scale_log2, 1.2e-38f);   // a scale of 0 weighs all rows alike; -inf stays -inf
-    bool ok = true;
-    Turn n;
-    Peek ahead = peek(p, static_cast<int>(blockIdx.x >> 1));
-    for (int item = static_cast<int>(blockIdx.x >> 1); item < p.items; item += static_cast<int>(gridDim.x >> 1)) {
-    const Work w = work_of(p, item, ahead);
-    if (tid == 0 && rank == 0 && (ahead.seq < 0 || ahead.seq >= a.nseq)) record_error(err, MISA_DEVERR_BAD_SEQ);
-    ahead = peek(p, item + static_cast<int>(gridDim.x >> 1));
-    const int ntiles = w.tile1 - w.tile0;
-    float m = kNegInf, l = 0.f;
-    int32_t here = ntiles > 0 ? row_of(w, w.tile0 * kTile + half * 32 + lane) : -1;   // this lane's row of the half
-    for (int i = 0; i < ntiles; ++i, ++n.n) {
-      const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);   // rows of this half that exist
-      // a wait that gave up ends the work, not the loop: the warps' barriers stay paired
-      ok = ok && wait_warp(sb + kSFull + n.at(), n.parity(), err);
-      uint32_t s[32];
-      float mx = kNegInf;
-      if (ok) {
-        tc_fence_after();
-        tmem_ld32(t_lane + kTmemS + n.stage() * 32, s);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_in(sb + kSEmpty + n.at(), 0);
-        if (live != 0xffffffffu) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!((live >> j) & 1u)) s[j] = 0xff800000u;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
-      }
-      if (i + 1 < ntiles) here = row_of(w, (w.tile0 + i + 1) * kTile + half * 32 + lane);
-      // the other half of the tile's rows for the same head
-      const uint32_t red = sb + kOffRed + n.stage() * 512;
-      st_shared(red + tid * 4, __float_as_uint(mx));
-      named_bar_sync(1, 128);
-      mx = fmaxf(mx, __uint_as_float(ld_shared(red + (tid ^ 64) * 4))) * c;
-      float f = 1.f;
-      if (mx > m + 8.f || (m == kNegInf && mx > kNegInf)) {
-        f = m == kNegInf ? 0.f : ex2(m - mx);
-        m = mx;
-        l *= f;
-      }
-      const float mr = m == kNegInf ? 0.f : m;
-      float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {   // (the packed pairs take the place of the scores)
-        const float x = ex2(fmaf(__uint_as_float(s[j]), c, -mr)), y = ex2(fmaf(__uint_as_float(s[j + 1]), c, -mr));
-        l0 += x;
-        l1 += y;
-        s[j >> 1] = pack_bf16(x, y);
-      }
-      l += l0 + l1;
-      // P's stage is free once O of two tiles ago is done; O is scaled once the last one is
-      ok = ok && wait_warp(sb + kPvDone + n.at(), n.before(), err);
-      if (__any_sync(0xffffffffu, f != 1.f) && i > 0 && ok) {
-        Turn last = n;
-        --last.n;
-        ok = wait_warp(sb + kPvDone + last.at(), last.parity(), err);
-        tc_fence_after();
-#pragma unroll 1
-        for (int o = 0; o < 256; o += 16) {
-          uint32_t v[16];
-          tmem_ld16(t_lane + o, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-          tmem_st16(t_lane + o, v);
-        }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-      }
-      if (!ok) continue;
-      const uint32_t prow = sb + kOffP + n.stage() * kPStage + hl * 128;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        st_shared16(prow + (((half * 4 + u) ^ (hl & 7)) << 4), make_uint4(s[4 * u], s[4 * u + 1], s[4 * u + 2], s[4 * u + 3]));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_in(sb + kPFull + n.at(), 0);
-    }
-    Turn last = n;
-    --last.n;
-    if (ntiles > 0) {   // both halves' sums
-      st_shared(sb + kOffRed + 1024 + tid * 4, __float_as_uint(l));
-      named_bar_sync(1, 128);
-      l += __uint_as_float(ld_shared(sb + kOffRed + 1024 + (tid ^ 64) * 4));
-      ok = ok && wait_warp(sb + kPvDone + last.at(), last.parity(), err);
-      tc_fence_after();
-    }
-    // Output by 128 bytes a row: each warp turns its 32 heads' pieces round in its
-    // 4 KB of P (free until the next tile), so that eight lanes store a row's piece.
-    // (Stored straight from TMEM's lanes, each to a row of its own, an item's output
-    // took 4 us.)
-    const bool any = l > 0.f || l != l;
-    const int64_t row0 = (p.nsplit > 1 ? static_cast<int64_t>(w.t) * p.nsplit + w.split : static_cast<int64_t>(w.t)) * a.Hq;
-    const int h0 = static_cast<int>(rank) * kHeads + (warp & 1) * 32;   // first head of the warp
-    if (h < a.Hq && half == 0) {
-      if (p.nsplit > 1)
-        *reinterpret_cast<float2*>(p.part_ml + (row0 + h) * 2) = make_float2(any ? m : kNegInf, l);
-      else if (a.lse)
-        a.lse[row0 + h] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
-    }
-    const uint32_t turn = sb + kOffP + warp * 4096;
-    auto turned = [&](uint8_t* out, int64_t row_bytes) {   // out: where the first head's piece goes
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = j * 4 + (lane >> 3);
-        if (h0 + r < a.Hq)
-          *reinterpret_cast<uint4*>(out + r * row_bytes + (lane & 7) * 16) =
-              ld_shared16(turn + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-      }
-      __syncwarp();
-    };
-    const bool have = ntiles > 0 && ok;
-    if (p.nsplit > 1) {
-      uint8_t* out = reinterpret_cast<uint8_t*>(p.part_o + (row0 + h0) * kDv + half * 256);
-      if (have) {
-#pragma unroll 1
-        for (int o = 0; o < 256; o += 32) {
-          uint32_t v[32];
-          tmem_ld32(t_lane + o, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            st_shared16(turn + lane * 128 + ((j ^ (lane & 7)) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-          turned(out + o * 4, kDv * 4);
-        }
-      }
-    } else {
-      const float inv = any ? 1.f / l : 0.f;
-      uint8_t* out = reinterpret_cast<uint8_t*>(a.out + (row0 + h0) * kDv + half * 256);
-#pragma unroll 1
-      for (int o = 0; o < 256; o += 32) {
-        uint32_t v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = 0u;
-        if (have) {
-          tmem_ld32(t_lane + o, v);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t x[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            x[u] = pack_bf16(__uint_as_float(v[8 * j + 2 * u]) * inv, __uint_as_float(v[8 * j + 2 * u + 1]) * inv);
-          st_shared16(turn + lane * 128 + ((((o >> 3) & 4) + j) ^ (lane & 7)) * 16, make_uint4(x[0], x[1], x[2], x[3]));
-        }
-        if (o & 32) turned(out + (o - 32) * 2, kDv * 2);
-      }
-    }
-    if (ntiles > 0 && ok) {   // O has been read
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_in(sb + kOEmpty, 0);
-    }
-    }
+    softmax(p, rank, warp >> 2, tid & 127, tmem, sb);
   }
 
   tc_fence_before();
