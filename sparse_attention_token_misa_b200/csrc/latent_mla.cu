@@ -25,8 +25,8 @@
 //     through registers (rows of 64 entries in 128-byte swizzled atoms serve both
 //     products, K-major in one and MN-major in the other).  So a row is read from L2
 //     and widened once.  O stays in TMEM, 256 columns.
-// S has two places, so that the products of tile i + 1 run while the softmax of
-// tile i does.
+// S has four places, so that the products run ahead: a tile's way through softmax
+// and back takes about 2900 cycles (with two places the speed was half of that).
 //
 // What bounds a tile of bf16 rows is 74 KB a CTA from L2 (about 30 bytes a cycle:
 // 2500 cycles, and all rows twice would be 139 KB) and 32 KB to the other CTA (16
@@ -77,9 +77,9 @@ constexpr uint32_t kCopied = kKEmpty + 16;        // bf16: read by those that co
 constexpr uint32_t kVFull = kCopied + 16;         // first CTA: both CTAs' values are there
 constexpr uint32_t kVLanded = kVFull + 16;        // this CTA's values of the other one's rows
 constexpr uint32_t kVEmpty = kVLanded + 16;       // multiplied
-constexpr uint32_t kSFull = kVEmpty + 16;         // S complete
-constexpr uint32_t kSEmpty = kSFull + 16;         // first CTA: S read by both
-constexpr uint32_t kPFull = kSEmpty + 16;         // first CTA: P written (and O scaled) by both
+constexpr uint32_t kSFull = kVEmpty + 16;         // [4] S complete
+constexpr uint32_t kSEmpty = kSFull + 32;         // [4] first CTA: S read by both
+constexpr uint32_t kPFull = kSEmpty + 32;         // first CTA: P written (and O scaled) by both
 constexpr uint32_t kPvDone = kPFull + 16;         // O += P V complete
 constexpr uint32_t kOEmpty = kPvDone + 16;        // (one) first CTA: O of the item before read by both
 constexpr uint32_t kQFull = kOEmpty + 8;          // (one) this CTA's queries landed
@@ -92,9 +92,9 @@ constexpr uint32_t kOffRef = kOffMax + 1024;      // [2][64]: a head's reference
 constexpr uint32_t kOffSum = kOffRef + 512;       // [2][128]: an item's sums of the warpgroup that does not finish it
 constexpr int kSmemBytes = kOffSum + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-// Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-19 the rest.
-constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps, kThreads = (kMmaWarp + 4) * 32;
-constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: two places of 32 columns
+// Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-20 the rest.
+constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps, kThreads = (kMmaWarp + 5) * 32;
+constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: four places of 32 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 64);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
 
@@ -367,6 +367,10 @@ struct Turn {
   __device__ __forceinline__ uint32_t stage() const { return n & 1; }
   __device__ __forceinline__ uint32_t parity() const { return (n >> 1) & 1; }   // of the phase that ends with this tile
   __device__ __forceinline__ uint32_t before() const { return parity() ^ 1u; }  // of the one that ended two tiles ago
+  // The same of S, which has four places.
+  __device__ __forceinline__ uint32_t at4() const { return 8 * (n & 3); }
+  __device__ __forceinline__ uint32_t place4() const { return n & 3; }
+  __device__ __forceinline__ uint32_t parity4() const { return (n >> 2) & 1; }
 };
 
 // Brings quantised rows, 256 threads: thread = (row r0, piece of 8 entries) of each
@@ -397,24 +401,25 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, in
 #pragma unroll 1
     for (int tile = w.tile0 - 1; tile < w.tile1; ++tile) {
       const bool real = tile >= w.tile0;
-      if (real && !(wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err) && wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)))
-        return;
+      if (real && !wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return;
       if (piece == 0 && (id < -1 || id >= w.L)) record_error(p.a.err, MISA_DEVERR_BAD_INDEX);
       const bool here = id >= 0 && id < w.L;
       const uint8_t* src = w.base + static_cast<int64_t>(here ? id : 0) * kRow;   // of the next tile
       const uint32_t kdst = kdst0 + n.stage() * kKStage, vofs = n.stage() * kVStage, far_bar = far_bar0 + n.at();
+      uint4 y[8];
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         const uint32_t word = b < 2 ? scale.x : b < 4 ? scale.y : b < 6 ? scale.z : scale.w;
-        const uint4 y = kv_decode8<kFmt>(code[b].x, code[b].y, kv_scale(__byte_perm(word, 0u, sel + 2 * (b & 1))));
-        if (real) {
-          st_shared16(kdst + b * kKBlock, y);
-          if ((b >> 2) == static_cast<int>(rank)) st_shared16(vdst0 + vofs + (b & 3) * kVBlock, y);
-          else st_async16(far0 + vofs + (b & 3) * kVBlock, y, far_bar);
-        }
+        y[b] = kv_decode8<kFmt>(code[b].x, code[b].y, kv_scale(__byte_perm(word, 0u, sel + 2 * (b & 1))));
+        if (real) st_shared16(kdst + b * kKBlock, y[b]);
         code[b] = load_code<kFmt>(src, b * 64 + piece * 8);
       }
-      if (real) st_shared16(kdst + 8 * kKBlock, rope);
+      if (real) {
+        st_shared16(kdst + 8 * kKBlock, rope);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) arrive_in(sb + kKFull + n.at(), 0);
+      }
       scale = rope = make_uint4(0u, 0u, 0u, 0u);
       if (here) {
         scale = __ldg(reinterpret_cast<const uint4*>(src + kv_code_bytes(kFmt)));
@@ -422,12 +427,15 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, in
       }
       load_id(tile + 2);
       if (real) {
+        if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          if ((b >> 2) == static_cast<int>(rank)) st_shared16(vdst0 + vofs + (b & 3) * kVBlock, y[b]);
+          else st_async16(far0 + vofs + (b & 3) * kVBlock, y[b], far_bar);
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-          arrive_in(sb + kKFull + n.at(), 0);
-          arrive_in(sb + kVFull + n.at(), 0);
-        }
+        if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + n.at(), 0);
         ++n.n;
       }
     }
@@ -567,66 +575,23 @@ __device__ __forceinline__ void pass_rows(const MlaParams& p, uint32_t sb) {
   }
 }
 
-// Issues the products of both CTAs, a warp of the first.  Two rows of work over the
-// items, S of one tile after the other and O += P V; whichever has its operands next
-// is issued, O first.  The warp looks at all the barriers together, and one lane
-// issues a tile's.
-__device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint32_t sb) {
+// Issue the products of both CTAs, two warps of the first: S of one tile after the
+// other, and O += P V.  Each waits for its own operands; the tensor core takes what
+// comes first.  (One warp for both had to look at six barriers in turn, at 50 to 90
+// cycles each: it saw an operand 300 to 800 cycles late.)  All lanes wait, one issues.
+__device__ __forceinline__ void multiply_rows(const MlaParams& p, uint32_t tmem, uint32_t sb) {
   const bool leader = elect_one();
-  Items si(p), oi(p);
-  int s_left = 0, o_left = 0;           // tiles of the item at hand
-  bool s_any = true, s_first = false, o_first = false;
-  Turn s, o;
-  uint32_t s_items = 0, o_items = 0;    // items begun
-  uint32_t t0 = clock();
-  while (true) {
-    if (s_left == 0 && s_any) {
-      s_any = si.next(p);
-      s_left = s_any ? si.w.tile1 - si.w.tile0 : 0;
-      s_first = true;
-      s_items += s_any;
-    }
-    if (o_left == 0) {
-      if (!oi.next(p)) break;
-      o_left = oi.w.tile1 - oi.w.tile0;
-      o_first = true;
-      ++o_items;
-    }
-    uint32_t ready = test_phase(sb + kPFull + o.at(), o.parity());
-    ready |= test_phase(sb + kVFull + o.at(), o.parity()) << 1;
-    ready |= test_phase(sb + kOEmpty, o_items & 1) << 2;               // the item before's (o_items - 2)
-    ready |= test_phase(sb + kSEmpty + s.at(), s.before()) << 3;
-    ready |= test_phase(sb + kKFull + s.at(), s.parity()) << 4;
-    ready |= test_phase(sb + kQReady, (s_items - 1) & 1) << 5;
-    ready = __reduce_and_sync(0xffffffffu, ready);
-    if (!o_first || o_items == 1) ready |= 4u;
-    if (!s_first) ready |= 32u;
-    if (o.n < s.n && (ready & 7u) == 7u) {
+  Turn n;
+  uint32_t items = 0;
+  for (Items it(p); it.next(p); ++items) {
+    if (!wait_warp(sb + kQReady, items & 1, p.a.err)) break;
+#pragma unroll 1
+    for (int left = it.w.tile1 - it.w.tile0; left > 0; --left, ++n.n) {
+      if (!wait_warp(sb + kSEmpty + n.at4(), n.parity4() ^ 1u, p.a.err) || !wait_warp(sb + kKFull + n.at(), n.parity(), p.a.err)) goto done;
       if (leader) {
         tc_fence_after();
-        const uint64_t w = sw128_kmajor_desc(sb + kOffP + o.stage() * kPStage);
-        const uint64_t v = sw128_mnmajor_desc(sb + kOffV + o.stage() * kVStage, kVBlock);
-        const uint32_t add = !o_first;
-        umma_pair<0, 0>(tmem, w, v, kIdescO, add);                      // 16 rows, entries 0 .. 127 of each half
-        umma_pair<0, 2 * kVBlock>(tmem + 128, w, v, kIdescO, add);
-        umma_pair<32, 2048>(tmem, w, v, kIdescO, 1);
-        umma_pair<32, 2 * kVBlock + 2048>(tmem + 128, w, v, kIdescO, 1);
-        umma_pair<64, 4096>(tmem, w, v, kIdescO, 1);
-        umma_pair<64, 2 * kVBlock + 4096>(tmem + 128, w, v, kIdescO, 1);
-        umma_pair<96, 6144>(tmem, w, v, kIdescO, 1);
-        umma_pair<96, 2 * kVBlock + 6144>(tmem + 128, w, v, kIdescO, 1);
-        commit_pair(sb + kVEmpty + o.at());
-        commit_pair(sb + kPvDone + o.at());
-      }
-      ++o.n;
-      --o_left;
-      o_first = false;
-      t0 = clock();
-    } else if (s_left && s.n < o.n + 2 && (ready & 56u) == 56u) {
-      if (leader) {
-        tc_fence_after();
-        const uint32_t d = tmem + kTmemS + s.stage() * 32;
-        uint64_t q = sw128_kmajor_desc(sb + kOffQ), k = sw128_kmajor_desc(sb + kOffK + s.stage() * kKStage);
+        const uint32_t d = tmem + kTmemS + n.place4() * 32;
+        uint64_t q = sw128_kmajor_desc(sb + kOffQ), k = sw128_kmajor_desc(sb + kOffK + n.stage() * kKStage);
         uint32_t add = 0;
 #pragma unroll 1
         for (int b = 0; b < kBlocks; b += 3) {
@@ -646,20 +611,46 @@ __device__ __forceinline__ void multiply(const MlaParams& p, uint32_t tmem, uint
           q += 3 * kQBlock >> 4;
           k += 3 * kKBlock >> 4;
         }
-        commit_pair(sb + kKEmpty + s.at());
-        commit_pair(sb + kSFull + s.at());
-        if (s_left == 1) commit_pair(sb + kQEmpty);
+        commit_pair(sb + kSFull + n.at4());
+        commit_pair(sb + kKEmpty + n.at());
+        if (left == 1) commit_pair(sb + kQEmpty);
       }
-      ++s.n;
-      --s_left;
-      s_first = false;
-      t0 = clock();
-    } else if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) {
-      record_error(p.a.err, MISA_DEVERR_TIMEOUT);
-      break;
+      __syncwarp();
     }
-    __syncwarp();
   }
+done:
+  if (leader) commit_pair(sb + kDone);
+  __syncwarp();
+}
+__device__ __forceinline__ void multiply_values(const MlaParams& p, uint32_t tmem, uint32_t sb) {
+  const bool leader = elect_one();
+  Turn n;
+  uint32_t items = 0;
+  for (Items it(p); it.next(p); ++items) {
+    if (!wait_warp(sb + kOEmpty, (items & 1) ^ 1u, p.a.err)) break;
+#pragma unroll 1
+    for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
+      if (!wait_warp(sb + kVFull + n.at(), n.parity(), p.a.err) || !wait_warp(sb + kPFull + n.at(), n.parity(), p.a.err)) goto done;
+      if (leader) {
+        tc_fence_after();
+        const uint64_t w = sw128_kmajor_desc(sb + kOffP + n.stage() * kPStage);
+        const uint64_t v = sw128_mnmajor_desc(sb + kOffV + n.stage() * kVStage, kVBlock);
+        const uint32_t add = tile > it.w.tile0;
+        umma_pair<0, 0>(tmem, w, v, kIdescO, add);                      // 16 rows, entries 0 .. 127 of each half
+        umma_pair<0, 2 * kVBlock>(tmem + 128, w, v, kIdescO, add);
+        umma_pair<32, 2048>(tmem, w, v, kIdescO, 1);
+        umma_pair<32, 2 * kVBlock + 2048>(tmem + 128, w, v, kIdescO, 1);
+        umma_pair<64, 4096>(tmem, w, v, kIdescO, 1);
+        umma_pair<64, 2 * kVBlock + 4096>(tmem + 128, w, v, kIdescO, 1);
+        umma_pair<96, 6144>(tmem, w, v, kIdescO, 1);
+        umma_pair<96, 2 * kVBlock + 6144>(tmem + 128, w, v, kIdescO, 1);
+        commit_pair(sb + kVEmpty + n.at());
+        commit_pair(sb + kPvDone + n.at());
+      }
+      __syncwarp();
+    }
+  }
+done:
   if (leader) commit_pair(sb + kDone);
   __syncwarp();
 }
@@ -720,18 +711,17 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
 #pragma unroll 1
     for (; n.n < end; n.n += 2) {
       const uint32_t live = __ballot_sync(0xffffffffu, here >= 0);   // rows of this half that exist
-      // A wait that gave up ends the work, not the loop: the barriers stay paired.  S
-      // complete also says that O of two tiles ago is, which read this place of P.
-      ok = ok && wait_warp(sb + kSFull + n.at(), n.parity(), err);
+      // A wait that gave up ends the work, not the loop: the barriers stay paired.
+      ok = ok && wait_warp(sb + kSFull + n.at4(), n.parity4(), err);
       uint32_t s[32];
       float mx = kNegInf;
       if (ok) {
         tc_fence_after();
-        tmem_ld32(t_lane + kTmemS + group * 32, s);
+        tmem_ld32(t_lane + kTmemS + n.place4() * 32, s);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_in(sb + kSEmpty + n.at(), 0);
+        if (lane == 0) arrive_in(sb + kSEmpty + n.at4(), 0);
         if (live != 0xffffffffu) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -771,6 +761,7 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
         s[j >> 1] = pack_bf16(x, y);
       }
       l += l0 + l1;
+      ok = ok && wait_warp(sb + kPvDone + n.at(), n.before(), err);   // O of two tiles ago has read this place of P
       if (!ok) continue;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -890,8 +881,10 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       bar_init(sb + kVFull + at, 2 * (kRowWarps + 1));                // and pass_values
       bar_init(sb + kVLanded + at, 1);
       bar_init(sb + kVEmpty + at, 1);
-      bar_init(sb + kSFull + at, 1);
-      bar_init(sb + kSEmpty + at, 8);
+      for (uint32_t two = 0; two < 32; two += 16) {
+        bar_init(sb + kSFull + two + at, 1);
+        bar_init(sb + kSEmpty + two + at, 8);
+      }
       bar_init(sb + kPFull + at, 8);
       bar_init(sb + kPvDone + at, 1);
     }
@@ -899,7 +892,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     bar_init(sb + kQFull, 1);
     bar_init(sb + kQReady, 2);
     bar_init(sb + kQEmpty, 1);
-    bar_init(sb + kDone, 1);
+    bar_init(sb + kDone, 2);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -921,9 +914,11 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   const LatentArgs& a = p.a;
   uint32_t* err = a.err;
   if (warp == kMmaWarp) {
-    if (rank == 0) multiply(p, tmem, sb);
+    if (rank == 0) multiply_rows(p, tmem, sb);
     wait_all(sb, err);   // nothing reads this CTA's memory any more
     __syncwarp();
+  } else if (warp == kMmaWarp + 4) {
+    if (rank == 0) multiply_values(p, tmem, sb);
   } else if (warp == kMmaWarp + 1) {
     pass_values(p, lane, sb);
   } else if (warp == kMmaWarp + 2) {
