@@ -18,6 +18,7 @@ from ._native import MLA_DQK, MLA_DV, _call, _p, _req, _shape
 
 KV_FORMS = {"bf16": 0, "mx8": 1, "mx4": 2}       # MISA_KV_BF16, MISA_KV_MX8, MISA_KV_MX4
 _ROW_BYTES = {"bf16": 1152, "mx8": 656, "mx4": 400}
+_FORM_OF = {(torch.bfloat16, MLA_DQK): "bf16", (torch.uint8, 656): "mx8", (torch.uint8, 400): "mx4"}
 
 
 def kv_row_bytes(form: str) -> int:
@@ -36,13 +37,11 @@ def alloc_kv_cache(nseq: int, L: int, form: str, device=None) -> torch.Tensor:
 
 
 def _cache_form(cache: torch.Tensor) -> str:
-    if cache.dim() == 3:
-        for form, nbytes in _ROW_BYTES.items():
-            want = (torch.bfloat16, MLA_DQK) if form == "bf16" else (torch.uint8, nbytes)
-            if (cache.dtype, cache.shape[2]) == want:
-                if cache.stride(2) != 1 or cache.stride(1) != cache.shape[2]:
-                    raise ValueError("cache rows must be contiguous and follow one another")
-                return form
+    form = _FORM_OF.get((cache.dtype, cache.shape[2])) if cache.dim() == 3 else None
+    if form is not None:
+        if cache.stride(2) != 1 or cache.stride(1) != cache.shape[2]:
+            raise ValueError("cache rows must be contiguous and follow one another")
+        return form
     raise ValueError("cache: expected shape [nseq, L, 576] bf16 or [nseq, L, 656 or 400] uint8, got "
                      f"{tuple(cache.shape)} {cache.dtype}")
 
@@ -56,20 +55,27 @@ def _idx_stride(idx: torch.Tensor) -> int:
     return int(idx.stride(0)) if idx.shape[0] > 1 else idx.shape[1]
 
 
-@contextlib.contextmanager
 def _on(first: torch.Tensor, stream, *others):
-    """The device of `first` made current (the library launches there; every
-    tensor has to be on it), and `stream`, so that what a call allocates for
-    itself belongs to the stream that uses it."""
+    """A context with the device of `first` made current (the library launches
+    there; every tensor has to be on it), and `stream`, so that what a call
+    allocates for itself belongs to the stream that uses it."""
     _p(first)
+    device = first.get_device()
     for t in others:
-        if t is not None and (_p(t), t.device)[1] != first.device:
+        if t is not None and (_p(t), t.get_device())[1] != device:
             raise ValueError(f"tensors on {first.device} and {t.device}")
-    with torch.cuda.device(first.device):
+    if stream is None and device == torch.cuda.current_device():
+        return contextlib.nullcontext(torch.cuda.current_stream(device).cuda_stream)
+    return _switched(first.device, stream)
+
+
+@contextlib.contextmanager
+def _switched(device: torch.device, stream):
+    with torch.cuda.device(device):
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=first.device)
-        if stream is not None and stream.device != first.device:
-            raise ValueError(f"tensors on {first.device}, stream on {stream.device}")
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"tensors on {device}, stream on {stream.device}")
         with torch.cuda.stream(stream):
             yield torch.cuda.current_stream().cuda_stream
 
