@@ -93,7 +93,8 @@ constexpr uint32_t kOffSum = kOffRef + 512;       // [2][128]: an item's sums of
 constexpr int kSmemBytes = kOffSum + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-20 the rest.
-constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps, kThreads = (kMmaWarp + 5) * 32;
+constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps;
+constexpr int mla_threads(int fmt) { return (kMmaWarp + (fmt == MISA_KV_BF16 ? 5 : 4)) * 32; }
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: four places of 32 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 64);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -207,7 +208,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // One product with operands kA and kB bytes behind those of the descriptors (added
 // here: worked out ahead of the loop, the descriptors of a tile fill the registers).
@@ -280,7 +281,7 @@ struct MlaParams {
   LatentArgs a;
   int nsplit, items; // items: T * nsplit
   uint32_t by_nsplit;   // ceil(2^32 / nsplit) (nsplit > 1)
-  float* part_o;     // [T][nsplit][Hq][512] (nsplit > 1)
+  float* part_o;     // [T][nsplit][512 / 4][Hq][4] (nsplit > 1)
   float* part_ml;    // [T][nsplit][Hq][2]: m (log2 units), l
 };
 // An item: tiles [tile0, tile1) of the n row slots of query t.
@@ -812,51 +813,59 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
     last.n = end - 1;
     ok = ok && wait_warp(sb + kPvDone + last.at(), last.parity(), err);
     tc_fence_after();
-    // Output: each warp turns its 32 heads' pieces round in its 2 KB of this
-    // warpgroup's place of P, so that four lanes store 64 bytes of a row.  (Stored
-    // straight from TMEM's lanes, each to a row of its own, an item's output took 4 us.)
+    // Output, 16 entries of O at a time.  Partial sums go out as they lie, a head a
+    // lane (the scratch has the heads side by side).  For bf16 each warp turns its 32
+    // heads' pieces round in its 2 KB of this warpgroup's place of P, so that four lanes
+    // store 64 bytes of a row, while the next entries come from TMEM.
     const bool any = l > 0.f || l != l;
     if (h < a.Hq && half == 0) {
       if (p.nsplit > 1) *reinterpret_cast<float2*>(p.part_ml + (row0 + h) * 2) = make_float2(any ? m : kNegInf, l);
       else if (a.lse) a.lse[row0 + h] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
     }
-    const uint32_t turn_p = my_p + warp * 2048;
-    const bool part = p.nsplit > 1;
-    const float inv = part ? 1.f : any ? 1.f / l : 0.f;
-    const int64_t row_bytes = part ? kDv * 4 : kDv * 2;
-    uint8_t* out = (part ? reinterpret_cast<uint8_t*>(p.part_o) : reinterpret_cast<uint8_t*>(a.out)) + (row0 + h0) * row_bytes +
-                   half * (row_bytes / 2) + (lane & 3) * 16;
-    const int rows = ok ? min(32, a.Hq - h0) : 0;
+    uint32_t v[16];
+    tmem_ld16(t_lane, v);
+    if (p.nsplit > 1) {
+      float4* out = reinterpret_cast<float4*>(p.part_o) + row0 * (kDv / 4) + static_cast<int64_t>(half) * 64 * a.Hq + h;
 #pragma unroll 1
-    for (int o = 0; o < 256; o += 16) {
-      uint32_t v[16];
-      tmem_ld16(t_lane + o, v);
-      tmem_wait_ld();
-      // 16 entries a lane: 64 bytes as they are, or with the next 16 as bf16
-      const uint32_t at = turn_p + lane * 64, swz = (lane >> 1) & 3;
-      if (part) {
+      for (int o = 16; o <= 256; o += 16) {
+        tmem_wait_ld();
+        if (ok && h < a.Hq) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          st_shared16(at + ((j ^ swz) << 4), make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t x[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            x[u] = pack_bf16(__uint_as_float(v[8 * j + 2 * u]) * inv, __uint_as_float(v[8 * j + 2 * u + 1]) * inv);
-          st_shared16(at + ((((o >> 3) & 2) + j) ^ swz) * 16, make_uint4(x[0], x[1], x[2], x[3]));
+          for (int j = 0; j < 4; ++j)
+            out[j * a.Hq] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]), __uint_as_float(v[4 * j + 2]),
+                                        __uint_as_float(v[4 * j + 3]));
         }
-        if (!(o & 16)) continue;
+        out += 4 * a.Hq;
+        __syncwarp();
+        if (o < 256) tmem_ld16(t_lane + o, v);
       }
-      __syncwarp();
+    } else {
+      const uint32_t turn_p = my_p + warp * 2048, at = turn_p + lane * 64, swz = (lane >> 1) & 3;
+      const float inv = any ? 1.f / l : 0.f;
+      uint8_t* out = reinterpret_cast<uint8_t*>(a.out + (row0 + h0) * kDv + half * 256) + (lane >> 2) * (kDv * 2) + (lane & 3) * 16;
+      const int rows = ok ? a.Hq - h0 - (lane >> 2) : 0;   // from this lane's first on
+#pragma unroll 1
+      for (int o = 16; o <= 256; o += 16) {
+        tmem_wait_ld();
+        uint32_t x[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = j * 8 + (lane >> 2);
-        if (r < rows) *reinterpret_cast<uint4*>(out + r * row_bytes) = ld_shared16(turn_p + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+        for (int j = 0; j < 8; ++j) x[j] = pack_bf16(__uint_as_float(v[2 * j]) * inv, __uint_as_float(v[2 * j + 1]) * inv);
+        if (o < 256) tmem_ld16(t_lane + o, v);
+        const uint32_t second = ((o >> 3) & 2) ^ 2;   // 32 entries a store
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          st_shared16(at + (((second + j) ^ swz) << 4), make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+        if (!second) continue;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = j * 8 + (lane >> 2);
+          if (j * 8 < rows)
+            *reinterpret_cast<uint4*>(out + j * 8 * kDv * 2) = ld_shared16(turn_p + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+        }
+        out += 64;
+        __syncwarp();
       }
-      out += 64;
-      __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
@@ -865,7 +874,7 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(mla_threads(kFmt), 1) __cluster_dims__(2, 1, 1)
 latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap row_map, const MlaParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];   // swizzled operands
   const uint32_t sb = smem_u32(smem_raw);
@@ -905,7 +914,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();   // the other CTA's barriers are ready for arrivals
+  cluster_sync_all();   // the other CTA's barriers (fence_mbar_init) are ready for arrivals
   tc_fence_after();
   const uint32_t tmem = ld_shared(sb + kOffTmem);
   pdl_wait_inputs();
@@ -917,7 +926,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     if (rank == 0) multiply_rows(p, tmem, sb);
     wait_all(sb, err);   // nothing reads this CTA's memory any more
     __syncwarp();
-  } else if (warp == kMmaWarp + 4) {
+  } else if (warp == kMmaWarp + 3) {
     if (rank == 0) multiply_values(p, tmem, sb);
   } else if (warp == kMmaWarp + 1) {
     pass_values(p, lane, sb);
@@ -928,7 +937,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       if (elect_one()) ask_rows(p, rank, &q_map, &row_map, sb);
       __syncwarp();
     }
-  } else if (warp == kMmaWarp + 3) {
+  } else if (warp == kMmaWarp + 4) {
     if constexpr (!kQuant) {
       if (elect_one()) pass_rows(p, sb);
       __syncwarp();
@@ -948,44 +957,73 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the splits of a query: out[t, h] = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c
-// in split order.  One CTA of 128 threads per (t, h), 4 entries a thread.
+// Joins the splits of a query: out[t, h] = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c.
+// A CTA takes 8 heads and 32 entries: a thread 4 entries of every fourth split, in
+// order, then the four sums in order.  (All splits in one thread took twice as long
+// at 74 of them.)
 constexpr int kMaxSplits = 128;
-__global__ void __launch_bounds__(128)
+constexpr int kJoinHeads = 8, kJoinEntries = 32, kJoinParts = 4;
+__global__ void __launch_bounds__(kJoinHeads * kJoinEntries / 4 * kJoinParts)
 latent_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int Hq, int nsplit,
                    uint16_t* __restrict__ out, float* __restrict__ lse) {
-  __shared__ float sM[kMaxSplits], sL[kMaxSplits];
+  constexpr int kThreads = kJoinHeads * kJoinEntries / 4 * kJoinParts, kWidth = kThreads / kJoinParts;
+  __shared__ float sW[kJoinHeads][kMaxSplits + 1], sL[kJoinHeads][kMaxSplits + 1];
+  __shared__ float4 sO[kJoinParts - 1][kWidth];
   pdl_wait_inputs();
   pdl_allow_next();
-  const int t = static_cast<int>(blockIdx.x) / Hq, h = static_cast<int>(blockIdx.x) - t * Hq;
+  const int groups = (Hq + kJoinHeads - 1) / kJoinHeads;
+  const int e0 = static_cast<int>(blockIdx.x % (kDv / kJoinEntries)) * kJoinEntries;
+  const int t = static_cast<int>(blockIdx.x / (kDv / kJoinEntries)) / groups;
+  const int h0 = (static_cast<int>(blockIdx.x / (kDv / kJoinEntries)) - t * groups) * kJoinHeads;
   const int tid = threadIdx.x;
   const float kNegInf = -__int_as_float(0x7f800000);
-  const int64_t row0 = static_cast<int64_t>(t) * nsplit * Hq + h;
-  if (tid < nsplit) {
-    const float2 ml = *reinterpret_cast<const float2*>(part_ml + (row0 + static_cast<int64_t>(tid) * Hq) * 2);
-    sM[tid] = ml.x;
-    sL[tid] = ml.y;
+  const int64_t row0 = static_cast<int64_t>(t) * nsplit * Hq;
+  for (int x = tid; x < nsplit * kJoinHeads; x += kThreads) {
+    const int c = x / kJoinHeads, h = x % kJoinHeads;
+    const float2 ml = h0 + h < Hq ? *reinterpret_cast<const float2*>(part_ml + (row0 + static_cast<int64_t>(c) * Hq + h0 + h) * 2)
+                                  : make_float2(kNegInf, 0.f);
+    sW[h][c] = ml.x;
+    sL[h][c] = ml.y;
   }
   __syncthreads();
+  const int h = tid % kJoinHeads, e4 = e0 / 4 + (tid % kWidth) / kJoinHeads, part = tid / kWidth;
   float m = kNegInf;
-  for (int c = 0; c < nsplit; ++c) m = fmaxf(m, sM[c]);
-  float l = 0.f;
+  for (int c = 0; c < nsplit; ++c) m = fmaxf(m, sW[h][c]);
+  __syncthreads();
+  for (int c = tid / kJoinHeads; c < nsplit; c += kThreads / kJoinHeads)
+    // no rows: its O was not written; a sum without a maximum is NaN and stays so
+    sW[h][c] = sL[h][c] == 0.f ? 0.f : sW[h][c] == kNegInf ? 1.f : exp2f(sW[h][c] - m);
+  __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < nsplit; ++c) {
-    if (sL[c] == 0.f) continue;      // no rows: its O was not written
-    const float w = sM[c] == kNegInf ? 1.f : exp2f(sM[c] - m);   // a sum without a maximum is NaN and stays so
-    const float4 o = __ldcs(reinterpret_cast<const float4*>(part_o + (row0 + static_cast<int64_t>(c) * Hq) * kDv) + tid);
-    l += w * sL[c];
+  const float4* src = reinterpret_cast<const float4*>(part_o) + row0 * (kDv / 4) + static_cast<int64_t>(e4) * Hq + h0 + h;
+#pragma unroll 4
+  for (int c = part; c < nsplit; c += kJoinParts) {
+    if (sL[h][c] == 0.f) continue;
+    const float w = sW[h][c];
+    const float4 o = __ldcs(src + static_cast<int64_t>(c) * Hq * (kDv / 4));
     acc.x += w * o.x;
     acc.y += w * o.y;
     acc.z += w * o.z;
     acc.w += w * o.w;
   }
+  if (part) sO[part - 1][tid % kWidth] = acc;
+  __syncthreads();
+  if (part || h0 + h >= Hq) return;
+  float l = 0.f;
+  for (int c = 0; c < nsplit; ++c) l += sW[h][c] * sL[h][c];
+#pragma unroll
+  for (int u = 0; u < kJoinParts - 1; ++u) {
+    const float4 o = sO[u][tid];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
+  }
   const bool any = l > 0.f || l != l;
   const float inv = any ? 1.f / l : 0.f;
-  const int64_t row = static_cast<int64_t>(t) * Hq + h;
-  reinterpret_cast<uint2*>(out + row * kDv)[tid] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (lse && tid == 0) lse[row] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+  const int64_t row = static_cast<int64_t>(t) * Hq + h0 + h;
+  reinterpret_cast<uint2*>(out + row * kDv)[e4] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lse && e4 == 0) lse[row] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
 }
 
 // Clusters that run at once on the 148 SMs of a B200.
@@ -1039,9 +1077,10 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   p.items = a.T * p.nsplit;
   p.by_nsplit = p.nsplit > 1 ? static_cast<uint32_t>(((1ull << 32) + p.nsplit - 1) / p.nsplit) : 0u;
   const int clusters = p.items < kSlots ? p.items : kSlots;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(mla_threads(a.fmt)), kSmemBytes, stream, 0, qmap, rmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
-  return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * a.Hq), dim3(128), 0, stream, 0,
+  return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * ((a.Hq + kJoinHeads - 1) / kJoinHeads) * (kDv / kJoinEntries)),
+                    dim3(kJoinHeads * kJoinEntries / 4 * kJoinParts), 0, stream, 0,
                     static_cast<const float*>(p.part_o), static_cast<const float*>(p.part_ml), a.Hq, p.nsplit, a.out, a.lse);
 }
 
