@@ -70,7 +70,7 @@ constexpr uint32_t kOffK = kOffQ + kBlocks * kQBlock;   // [2]: stage = a tile's
 constexpr uint32_t kOffV = kOffK + 2 * kKStage;         // [2]
 constexpr uint32_t kOffP = kOffV + 2 * kVStage;         // [2]
 // barriers, one a stage (of the first CTA where it says so)
-constexpr uint32_t kKFull = kOffP + 2 * kPStage;  // first CTA: rows brought by both
+constexpr uint32_t kKFull = kOffP + 2 * kPStage;  // first CTA: quantised rows brought by both, bf16 ones by the other
 constexpr uint32_t kKHere = kKFull + 16;          // bf16: this CTA's rows landed
 constexpr uint32_t kKEmpty = kKHere + 16;         // multiplied
 constexpr uint32_t kCopied = kKEmpty + 16;        // bf16: read by those that copy to O's operand
@@ -83,7 +83,7 @@ constexpr uint32_t kPFull = kSEmpty + 32;         // first CTA: P written (and O
 constexpr uint32_t kPvDone = kPFull + 16;         // O += P V complete
 constexpr uint32_t kOEmpty = kPvDone + 16;        // (one) first CTA: O of the item before read by both
 constexpr uint32_t kQFull = kOEmpty + 8;          // (one) this CTA's queries landed
-constexpr uint32_t kQReady = kQFull + 8;          // (one) first CTA: both CTAs' queries landed
+constexpr uint32_t kQReady = kQFull + 8;          // (one) first CTA: queries landed (bf16: the other CTA's)
 constexpr uint32_t kQEmpty = kQReady + 8;         // (one) the item's last S complete
 constexpr uint32_t kDone = kQEmpty + 8;           // (one) every MMA retired
 constexpr uint32_t kOffTmem = kDone + 8;
@@ -94,7 +94,7 @@ constexpr int kSmemBytes = kOffSum + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-20 the rest.
 constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps;
-constexpr int mla_threads(int fmt) { return (kMmaWarp + (fmt == MISA_KV_BF16 ? 5 : 4)) * 32; }
+constexpr int kThreads = (kMmaWarp + 4) * 32;
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: four places of 32 columns
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 64);
 constexpr uint32_t kIdescO = idesc_bf16_f32(128, 256) | (1u << 16);   // values MN-major
@@ -561,7 +561,7 @@ __device__ __forceinline__ void ask_rows(const MlaParams& p, uint32_t rank, cons
     }
   }
 }
-// Passes on to the first CTA what has landed, one thread.
+// Passes on to the first CTA what has landed in the second, one thread.
 __device__ __forceinline__ void pass_rows(const MlaParams& p, uint32_t sb) {
   uint32_t items = 0;
   Turn n;
@@ -580,15 +580,18 @@ __device__ __forceinline__ void pass_rows(const MlaParams& p, uint32_t sb) {
 // other, and O += P V.  Each waits for its own operands; the tensor core takes what
 // comes first.  (One warp for both had to look at six barriers in turn, at 50 to 90
 // cycles each: it saw an operand 300 to 800 cycles late.)  All lanes wait, one issues.
+template <bool kQuant>
 __device__ __forceinline__ void multiply_rows(const MlaParams& p, uint32_t tmem, uint32_t sb) {
   const bool leader = elect_one();
   Turn n;
   uint32_t items = 0;
   for (Items it(p); it.next(p); ++items) {
-    if (!wait_warp(sb + kQReady, items & 1, p.a.err)) break;
+    if (!wait_warp(sb + kQReady, items & 1, p.a.err) || (!kQuant && !wait_warp(sb + kQFull, items & 1, p.a.err))) break;
 #pragma unroll 1
     for (int left = it.w.tile1 - it.w.tile0; left > 0; --left, ++n.n) {
-      if (!wait_warp(sb + kSEmpty + n.at4(), n.parity4() ^ 1u, p.a.err) || !wait_warp(sb + kKFull + n.at(), n.parity(), p.a.err)) goto done;
+      if (!wait_warp(sb + kSEmpty + n.at4(), n.parity4() ^ 1u, p.a.err) || !wait_warp(sb + kKFull + n.at(), n.parity(), p.a.err) ||
+          (!kQuant && !wait_warp(sb + kKHere + n.at(), n.parity(), p.a.err)))
+        goto done;
       if (leader) {
         tc_fence_after();
         const uint32_t d = tmem + kTmemS + n.place4() * 32;
@@ -874,7 +877,7 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(mla_threads(kFmt), 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap row_map, const MlaParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];   // swizzled operands
   const uint32_t sb = smem_u32(smem_raw);
@@ -883,7 +886,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   const uint32_t rank = cluster_rank();
   if (tid == 0) {
     for (uint32_t at = 0; at < 16; at += 8) {
-      bar_init(sb + kKFull + at, kQuant ? 2 * (kRowWarps + 1) : 2);   // bring_rows and look_ahead, or pass_rows
+      bar_init(sb + kKFull + at, kQuant ? 2 * (kRowWarps + 1) : 1);   // bring_rows and look_ahead, or pass_rows
       bar_init(sb + kKHere + at, 1);
       bar_init(sb + kKEmpty + at, 1);
       bar_init(sb + kCopied + at, kRowWarps);
@@ -899,7 +902,7 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
     bar_init(sb + kOEmpty, 8);
     bar_init(sb + kQFull, 1);
-    bar_init(sb + kQReady, 2);
+    bar_init(sb + kQReady, kQuant ? 2 : 1);
     bar_init(sb + kQEmpty, 1);
     bar_init(sb + kDone, 2);
     fence_mbar_init();
@@ -923,11 +926,16 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   const LatentArgs& a = p.a;
   uint32_t* err = a.err;
   if (warp == kMmaWarp) {
-    if (rank == 0) multiply_rows(p, tmem, sb);
+    if (rank == 0) multiply_rows<kQuant>(p, tmem, sb);
     wait_all(sb, err);   // nothing reads this CTA's memory any more
     __syncwarp();
   } else if (warp == kMmaWarp + 3) {
-    if (rank == 0) multiply_values(p, tmem, sb);
+    if (rank == 0) {
+      multiply_values(p, tmem, sb);
+    } else if (!kQuant) {
+      if (elect_one()) pass_rows(p, sb);
+      __syncwarp();
+    }
   } else if (warp == kMmaWarp + 1) {
     pass_values(p, lane, sb);
   } else if (warp == kMmaWarp + 2) {
@@ -935,11 +943,6 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
       look_ahead<kFmt>(p, rank, lane, &q_map, sb);
     } else {
       if (elect_one()) ask_rows(p, rank, &q_map, &row_map, sb);
-      __syncwarp();
-    }
-  } else if (warp == kMmaWarp + 4) {
-    if constexpr (!kQuant) {
-      if (elect_one()) pass_rows(p, sb);
       __syncwarp();
     }
   } else if (warp >= kRowWarp0) {
@@ -1077,7 +1080,7 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   p.items = a.T * p.nsplit;
   p.by_nsplit = p.nsplit > 1 ? static_cast<uint32_t>(((1ull << 32) + p.nsplit - 1) / p.nsplit) : 0u;
   const int clusters = p.items < kSlots ? p.items : kSlots;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(mla_threads(a.fmt)), kSmemBytes, stream, 0, qmap, rmap, p);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * ((a.Hq + kJoinHeads - 1) / kJoinHeads) * (kDv / kJoinEntries)),
                     dim3(kJoinHeads * kJoinEntries / 4 * kJoinParts), 0, stream, 0,
