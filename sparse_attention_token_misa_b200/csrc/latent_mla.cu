@@ -284,7 +284,8 @@ struct MlaParams {
   float* part_o;     // [T][nsplit][512 / 4][Hq][4] (nsplit > 1)
   float* part_ml;    // [T][nsplit][Hq][2]: m (log2 units), l
 };
-// An item: tiles [tile0, tile1) of the n row slots of query t.
+// An item: tiles [tile0, tile1) of the n row slots of query t.  Items run from the last
+// query to the first: a prompt's later queries have more rows, and short lists end evenly.
 struct Work {
   int t, split;
   int n, tile0, tile1;
@@ -304,7 +305,7 @@ struct Peek {
 __device__ __forceinline__ Peek peek(const MlaParams& p, int item) {
   Peek k = {0, 0, 0};
   if (item < p.items) {
-    k.t = over_splits(p, item);
+    k.t = p.a.T - 1 - over_splits(p, item);
     k.seq = __ldg(p.a.seq_of + k.t);
     k.len = p.a.idx ? p.a.k : __ldg(p.a.prefix_len + k.t);
   }
@@ -313,7 +314,7 @@ __device__ __forceinline__ Peek peek(const MlaParams& p, int item) {
 __device__ __forceinline__ Work work_of(const MlaParams& p, int item, Peek k) {
   Work w;
   w.t = k.t;
-  w.split = item - k.t * p.nsplit;
+  w.split = item - (p.a.T - 1 - k.t) * p.nsplit;
   w.L = static_cast<int>(p.a.L);
   w.idx = p.a.idx ? p.a.idx + static_cast<int64_t>(w.t) * p.a.idx_stride : nullptr;
   w.n = p.a.idx ? k.len : max(min(k.len, w.L), 0);
@@ -961,27 +962,27 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 }
 
 // Joins the splits of a query: out[t, h] = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c.
-// A CTA takes 8 heads and 32 entries: a thread 4 entries of every fourth split, in
-// order, then the four sums in order.  (All splits in one thread took twice as long
-// at 74 of them.)
+// A CTA takes 8 heads; each of its threads 4 x 4 entries of all splits in order, or, of
+// many splits, 4 entries of every fourth, and then the four sums in order.
 constexpr int kMaxSplits = 128;
-constexpr int kJoinHeads = 8, kJoinEntries = 32, kJoinParts = 4;
-__global__ void __launch_bounds__(kJoinHeads * kJoinEntries / 4 * kJoinParts)
+constexpr int kJoinHeads = 8, kJoinThreads = 256;
+constexpr int join_steps(int parts) { return parts == 1 ? 4 : 1; }
+constexpr int join_entries(int parts) { return kJoinThreads / parts / kJoinHeads * 4 * join_steps(parts); }   // of a CTA
+template <int kParts>
+__global__ void __launch_bounds__(kJoinThreads)
 latent_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, int Hq, int nsplit,
                    uint16_t* __restrict__ out, float* __restrict__ lse) {
-  constexpr int kThreads = kJoinHeads * kJoinEntries / 4 * kJoinParts, kWidth = kThreads / kJoinParts;
+  constexpr int kSteps = join_steps(kParts), kEntries = join_entries(kParts), kWidth = kJoinThreads / kParts;
   __shared__ float sW[kJoinHeads][kMaxSplits + 1], sL[kJoinHeads][kMaxSplits + 1];
-  __shared__ float4 sO[kJoinParts - 1][kWidth];
+  __shared__ float4 sO[kParts][kWidth];
   pdl_wait_inputs();
   pdl_allow_next();
   const int groups = (Hq + kJoinHeads - 1) / kJoinHeads;
-  const int e0 = static_cast<int>(blockIdx.x % (kDv / kJoinEntries)) * kJoinEntries;
-  const int t = static_cast<int>(blockIdx.x / (kDv / kJoinEntries)) / groups;
-  const int h0 = (static_cast<int>(blockIdx.x / (kDv / kJoinEntries)) - t * groups) * kJoinHeads;
+  const int block = static_cast<int>(blockIdx.x / (kDv / kEntries)), t = block / groups, h0 = (block - t * groups) * kJoinHeads;
   const int tid = threadIdx.x;
   const float kNegInf = -__int_as_float(0x7f800000);
   const int64_t row0 = static_cast<int64_t>(t) * nsplit * Hq;
-  for (int x = tid; x < nsplit * kJoinHeads; x += kThreads) {
+  for (int x = tid; x < nsplit * kJoinHeads; x += kJoinThreads) {
     const int c = x / kJoinHeads, h = x % kJoinHeads;
     const float2 ml = h0 + h < Hq ? *reinterpret_cast<const float2*>(part_ml + (row0 + static_cast<int64_t>(c) * Hq + h0 + h) * 2)
                                   : make_float2(kNegInf, 0.f);
@@ -989,52 +990,68 @@ latent_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
     sL[h][c] = ml.y;
   }
   __syncthreads();
-  const int h = tid % kJoinHeads, e4 = e0 / 4 + (tid % kWidth) / kJoinHeads, part = tid / kWidth;
+  const int h = tid % kJoinHeads, part = tid / kWidth;
+  const int e4 = static_cast<int>(blockIdx.x % (kDv / kEntries)) * (kEntries / 4) + tid % kWidth / kJoinHeads;
   float m = kNegInf;
   for (int c = 0; c < nsplit; ++c) m = fmaxf(m, sW[h][c]);
   __syncthreads();
-  for (int c = tid / kJoinHeads; c < nsplit; c += kThreads / kJoinHeads)
+  for (int c = tid / kJoinHeads; c < nsplit; c += kJoinThreads / kJoinHeads)
     // no rows: its O was not written; a sum without a maximum is NaN and stays so
     sW[h][c] = sL[h][c] == 0.f ? 0.f : sW[h][c] == kNegInf ? 1.f : exp2f(sW[h][c] - m);
   __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* src = reinterpret_cast<const float4*>(part_o) + row0 * (kDv / 4) + static_cast<int64_t>(e4) * Hq + h0 + h;
+  float4 acc[kSteps];
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* src = reinterpret_cast<const float4*>(part_o) + row0 * (kDv / 4) + static_cast<int64_t>(e4) * Hq + h0 + h;   // (a head that is not there: every sum is 0)
+  constexpr int kStride = kWidth / kJoinHeads;   // of a thread's steps
 #pragma unroll 4
-  for (int c = part; c < nsplit; c += kJoinParts) {
-    if (sL[h][c] == 0.f) continue;
+  for (int c = part; c < nsplit; c += kParts) {
+    const bool some = sL[h][c] != 0.f;
     const float w = sW[h][c];
-    const float4 o = __ldcs(src + static_cast<int64_t>(c) * Hq * (kDv / 4));
-    acc.x += w * o.x;
-    acc.y += w * o.y;
-    acc.z += w * o.z;
-    acc.w += w * o.w;
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const float4 o = some ? __ldcs(src + (static_cast<int64_t>(c) * (kDv / 4) + u * kStride) * Hq) : make_float4(0.f, 0.f, 0.f, 0.f);
+      acc[u].x += w * o.x;
+      acc[u].y += w * o.y;
+      acc[u].z += w * o.z;
+      acc[u].w += w * o.w;
+    }
   }
-  if (part) sO[part - 1][tid % kWidth] = acc;
-  __syncthreads();
-  if (part || h0 + h >= Hq) return;
+  if constexpr (kParts > 1) {
+    sO[part][tid % kWidth] = acc[0];
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int u = 1; u < kParts; ++u) {
+      const float4 o = sO[u][tid];
+      acc[0].x += o.x;
+      acc[0].y += o.y;
+      acc[0].z += o.z;
+      acc[0].w += o.w;
+    }
+  }
+  if (h0 + h >= Hq) return;
   float l = 0.f;
   for (int c = 0; c < nsplit; ++c) l += sW[h][c] * sL[h][c];
-#pragma unroll
-  for (int u = 0; u < kJoinParts - 1; ++u) {
-    const float4 o = sO[u][tid];
-    acc.x += o.x;
-    acc.y += o.y;
-    acc.z += o.z;
-    acc.w += o.w;
-  }
   const bool any = l > 0.f || l != l;
   const float inv = any ? 1.f / l : 0.f;
   const int64_t row = static_cast<int64_t>(t) * Hq + h0 + h;
-  reinterpret_cast<uint2*>(out + row * kDv)[e4] = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u)
+    reinterpret_cast<uint2*>(out + row * kDv)[e4 + u * kStride] =
+        make_uint2(pack_bf16(acc[u].x * inv, acc[u].y * inv), pack_bf16(acc[u].z * inv, acc[u].w * inv));
   if (lse && e4 == 0) lse[row] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
 }
 
 // Clusters that run at once on the 148 SMs of a B200.
 constexpr int kSlots = 74;
 
-// How many items share a query's rows.  An item takes its tiles and about five
-// tiles' worth of queries and output, a join about four more at the end; the split
-// that makes the busiest cluster's list shortest is taken.
+// How many items share a query's rows: the split that makes the busiest cluster's list
+// shortest, counted in tiles.  An item more costs a cluster about as much as 16 tiles
+// (its queries, its output, and waiting for both), a join 6.  Measured: 64 queries of
+// 2048 mx8 rows 51 us whole and 69 in halves, 32 queries 49 and 40; 16 of 32,768 rows
+// 177 us in four parts and 187 in nine.
+constexpr int kItemTiles = 16, kJoinTiles = 6;
 int pick_splits(int T, int64_t n) {
   const int64_t tiles = (n + kTile - 1) / kTile;
   int best = 1;
@@ -1042,7 +1059,7 @@ int pick_splits(int T, int64_t n) {
   for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
     if (s > 1 && static_cast<int64_t>(T) * s > 4 * kSlots) break;
     const int64_t rounds = (static_cast<int64_t>(T) * s + kSlots - 1) / kSlots;
-    const int64_t cost = rounds * ((tiles + s - 1) / s + 5) + (s > 1 ? 4 : 0);
+    const int64_t cost = rounds * ((tiles + s - 1) / s + kItemTiles) + (s > 1 ? kJoinTiles : 0);
     if (best_cost < 0 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -1082,9 +1099,12 @@ cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {
   const int clusters = p.items < kSlots ? p.items : kSlots;
   e = launch_pdl(kern, dim3(static_cast<unsigned>(clusters) * 2), dim3(kThreads), kSmemBytes, stream, 0, qmap, rmap, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
-  return launch_pdl(latent_join_kernel, dim3(static_cast<unsigned>(a.T) * ((a.Hq + kJoinHeads - 1) / kJoinHeads) * (kDv / kJoinEntries)),
-                    dim3(kJoinHeads * kJoinEntries / 4 * kJoinParts), 0, stream, 0,
-                    static_cast<const float*>(p.part_o), static_cast<const float*>(p.part_ml), a.Hq, p.nsplit, a.out, a.lse);
+  // Many splits to few queries: more threads to each sum.
+  const int parts = p.nsplit > 8 ? 4 : 1;
+  return launch_pdl(parts == 4 ? latent_join_kernel<4> : latent_join_kernel<1>,
+                    dim3(static_cast<unsigned>(a.T) * ((a.Hq + kJoinHeads - 1) / kJoinHeads) * (kDv / join_entries(parts))),
+                    dim3(kJoinThreads), 0, stream, 0, static_cast<const float*>(p.part_o), static_cast<const float*>(p.part_ml),
+                    a.Hq, p.nsplit, a.out, a.lse);
 }
 
 }  // namespace misa
