@@ -376,10 +376,11 @@ struct Turn {
 };
 
 // Brings quantised rows, 256 threads: thread = (row r0, piece of 8 entries) of each
-// block.  A piece is widened once and written twice: to S's operand, and to O's in
-// the CTA that multiplies it.  An absent row is any row's codes with scales of zero.
-// Where a piece has been widened, the same piece of the next tile is asked for into
-// its registers.
+// block.  A piece is widened once and written twice: to S's operand and, as soon as
+// there is room, to O's in the CTA that multiplies it.  An absent row is any row's codes
+// with scales of zero.  The codes of the next tile are asked for as soon as the
+// registers are free: behind the first writes they came late (mx8, 16 x 32,768 rows:
+// 178 and 192 us).
 template <int kFmt>
 __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
@@ -391,55 +392,55 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, in
   Turn n;
   for (Items it(p); it.next(p);) {
     const Work& w = it.w;
-    int32_t id;
-    auto load_id = [&](int tile) {
-      const int s = tile * kTile + own;
-      id = tile < w.tile1 && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
-    };
     uint2 code[8];
     uint4 scale, rope;
-    load_id(w.tile0);
-    // The first turn only asks for the first tile.
-#pragma unroll 1
-    for (int tile = w.tile0 - 1; tile < w.tile1; ++tile) {
-      const bool real = tile >= w.tile0;
-      if (real && !wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return;
+    auto id_of = [&](int tile) {
+      const int s = tile * kTile + own;
+      return tile < w.tile1 && s < w.n ? w.idx ? __ldg(w.idx + s) : s : -1;
+    };
+    int32_t id = id_of(w.tile0);
+    auto load = [&](int tile) {   // ask for this thread's pieces of a tile, and for its row of the one behind
       if (piece == 0 && (id < -1 || id >= w.L)) record_error(p.a.err, MISA_DEVERR_BAD_INDEX);
       const bool here = id >= 0 && id < w.L;
-      const uint8_t* src = w.base + static_cast<int64_t>(here ? id : 0) * kRow;   // of the next tile
-      const uint32_t kdst = kdst0 + n.stage() * kKStage, vofs = n.stage() * kVStage, far_bar = far_bar0 + n.at();
-      uint4 y[8];
+      const uint8_t* src = w.base + static_cast<int64_t>(here ? id : 0) * kRow;
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const uint32_t word = b < 2 ? scale.x : b < 4 ? scale.y : b < 6 ? scale.z : scale.w;
-        y[b] = kv_decode8<kFmt>(code[b].x, code[b].y, kv_scale(__byte_perm(word, 0u, sel + 2 * (b & 1))));
-        if (real) st_shared16(kdst + b * kKBlock, y[b]);
-        code[b] = load_code<kFmt>(src, b * 64 + piece * 8);
-      }
-      if (real) {
-        st_shared16(kdst + 8 * kKBlock, rope);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) arrive_in(sb + kKFull + n.at(), 0);
-      }
+      for (int b = 0; b < 8; ++b) code[b] = load_code<kFmt>(src, b * 64 + piece * 8);
       scale = rope = make_uint4(0u, 0u, 0u, 0u);
       if (here) {
         scale = __ldg(reinterpret_cast<const uint4*>(src + kv_code_bytes(kFmt)));
         rope = __ldg(reinterpret_cast<const uint4*>(src + kv_rope_offset(kFmt) + piece * 16));
       }
-      load_id(tile + 2);
-      if (real) {
-        if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return;
+      id = id_of(tile + 1);
+    };
+    load(w.tile0);
+#pragma unroll 1
+    for (int tile = w.tile0; tile < w.tile1; ++tile, ++n.n) {
+      uint4 y[8];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          if ((b >> 2) == static_cast<int>(rank)) st_shared16(vdst0 + vofs + (b & 3) * kVBlock, y[b]);
-          else st_async16(far0 + vofs + (b & 3) * kVBlock, y[b], far_bar);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + n.at(), 0);
-        ++n.n;
+      for (int b = 0; b < 8; ++b) {
+        const uint32_t word = b < 2 ? scale.x : b < 4 ? scale.y : b < 6 ? scale.z : scale.w;
+        y[b] = kv_decode8<kFmt>(code[b].x, code[b].y, kv_scale(__byte_perm(word, 0u, sel + 2 * (b & 1))));
       }
+      const uint4 y8 = rope;
+      load(tile + 1);
+      if (!wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return;
+      const uint32_t kdst = kdst0 + n.stage() * kKStage;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) st_shared16(kdst + b * kKBlock, y[b]);
+      st_shared16(kdst + 8 * kKBlock, y8);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) arrive_in(sb + kKFull + n.at(), 0);
+      if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return;
+      const uint32_t vofs = n.stage() * kVStage, far_bar = far_bar0 + n.at();
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if ((b >> 2) == static_cast<int>(rank)) st_shared16(vdst0 + vofs + (b & 3) * kVBlock, y[b]);
+        else st_async16(far0 + vofs + (b & 3) * kVBlock, y[b], far_bar);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + n.at(), 0);
     }
   }
 }
