@@ -33,7 +33,7 @@
 // bytes a cycle: 2000), of quantised rows the widening as well; the products take
 // 2176 cycles of the tensor cores, the softmax 1500 of its warps.
 //
-// A cluster stays on its SMs and takes every 74th item (a query, or a part of its
+// A cluster stays on its SMs and takes one item in 74 (a query, or a part of its
 // rows), each role on its own: the rows of the next item come while the output of
 // this one leaves.  (A cluster an item spent 9 us on starting, queries and output
 // around 3 us a tile.)  Few queries: the rows of each are split over several
@@ -327,23 +327,36 @@ __device__ __forceinline__ Work work_of(const MlaParams& p, int item, Peek k) {
   w.tile1 = min(w.tile0 + share, tiles);
   return w;
 }
-// The items of a cluster that have rows, one after the other.
-struct Items {
-  int item, step;
-  Peek ahead;
-  Work w;
-  __device__ __forceinline__ explicit Items(const MlaParams& p) {
-    step = static_cast<int>(gridDim.x >> 1);
-    item = static_cast<int>(blockIdx.x >> 1) - step;
-    ahead = peek(p, item + step);
+// The items of a cluster, one after the other: there and back through the clusters, so
+// that the first does not have the longest of every round of a prompt.
+struct Round {
+  int item, hop, next_hop;
+  __device__ __forceinline__ Round() {
+    const int c = static_cast<int>(blockIdx.x >> 1), clusters = static_cast<int>(gridDim.x >> 1);
+    item = c;
+    hop = 2 * (clusters - c) - 1;
+    next_hop = 2 * c + 1;
   }
+  __device__ __forceinline__ void next() {
+    item += hop;
+    const int h = hop;
+    hop = next_hop;
+    next_hop = h;
+  }
+};
+// Those that have rows.
+struct Items {
+  Round r;        // of the item behind `w`
+  Peek ahead;     // ... and what it is
+  Work w;
+  __device__ __forceinline__ explicit Items(const MlaParams& p) { ahead = peek(p, r.item); }
   // On to the next one.
   __device__ __forceinline__ bool next(const MlaParams& p) {
     do {
-      item += step;
-      if (item >= p.items) return false;
-      w = work_of(p, item, ahead);
-      ahead = peek(p, item + step);
+      if (r.item >= p.items) return false;
+      w = work_of(p, r.item, ahead);
+      r.next();
+      ahead = peek(p, r.item);
     } while (w.tile1 == w.tile0);
     return true;
   }
@@ -548,8 +561,6 @@ __device__ __forceinline__ void ask_rows(const MlaParams& p, uint32_t rank, cons
   uint32_t items = 0;
   Turn n;
   for (Items it(p); it.next(p); ++items) {
-    if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
-    load_queries(p, rank, it.w.t, q_map, sb);
     for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
       const int row = tile * kTile + static_cast<int>(rank) * kRows;
       const uint32_t bar = sb + kKHere + n.at();
@@ -559,6 +570,10 @@ __device__ __forceinline__ void ask_rows(const MlaParams& p, uint32_t rank, cons
       for (int b = 0; b < kBlocks; ++b) {
         tma_3d(sb + kOffK + n.stage() * kKStage + b * kKBlock, map, bar, b * 64, row, it.w.seq);
         if (tile + kAhead < it.w.tile1) tma_l2_3d(map, b * 64, row + kAhead * kTile, it.w.seq);
+      }
+      if (tile == it.w.tile0) {   // the first rows need not wait for the place of the queries
+        if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
+        load_queries(p, rank, it.w.t, q_map, sb);
       }
     }
   }
@@ -687,12 +702,13 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
   bool ok = true;
   Turn n;
   uint32_t items = 0;                              // that have rows, so far
-  const int step = static_cast<int>(gridDim.x >> 1);
-  Peek ahead = peek(p, static_cast<int>(blockIdx.x >> 1));
-  for (int item = static_cast<int>(blockIdx.x >> 1); item < p.items; item += step) {
-    const Work w = work_of(p, item, ahead);
+  Round r;
+  Peek ahead = peek(p, r.item);
+  while (r.item < p.items) {
+    const Work w = work_of(p, r.item, ahead);
     if (tid == 0 && group == 0 && rank == 0 && (ahead.seq < 0 || ahead.seq >= a.nseq)) record_error(err, MISA_DEVERR_BAD_SEQ);
-    ahead = peek(p, item + step);
+    r.next();
+    ahead = peek(p, r.item);
     const int ntiles = w.tile1 - w.tile0;
     const int64_t row0 = (p.nsplit > 1 ? static_cast<int64_t>(w.t) * p.nsplit + w.split : static_cast<int64_t>(w.t)) * a.Hq;
     if (ntiles == 0) {   // no rows: zeros, and a sum of nothing
