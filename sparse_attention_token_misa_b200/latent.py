@@ -46,6 +46,17 @@ def _cache_form(cache: torch.Tensor) -> str:
                      f"{tuple(cache.shape)} {cache.dtype}")
 
 
+def _dims(t: torch.Tensor, name: str, *dims: int) -> None:
+    """_shape for sizes that are all known: one comparison where they fit."""
+    if t.shape != dims:
+        _shape(t, name, *dims)
+
+
+def _ptr(t):
+    """The address of a tensor that _on has looked at."""
+    return None if t is None else t.data_ptr()
+
+
 def _seq_stride(cache: torch.Tensor) -> int:
     return int(cache.stride(0)) * cache.element_size() if cache.shape[0] > 1 else 0
 
@@ -59,10 +70,12 @@ def _on(first: torch.Tensor, stream, *others):
     """A context with the device of `first` made current (the library launches
     there; every tensor has to be on it), and `stream`, so that what a call
     allocates for itself belongs to the stream that uses it."""
-    _p(first)
     device = first.get_device()
+    if device < 0:
+        _p(first)
     for t in others:
-        if t is not None and (_p(t), t.get_device())[1] != device:
+        if t is not None and t.get_device() != device:
+            _p(t)
             raise ValueError(f"tensors on {first.device} and {t.device}")
     if stream is None and device == torch.cuda.current_device():
         return contextlib.nullcontext(torch.cuda.current_stream(device).cuda_stream)
@@ -90,15 +103,16 @@ def append_kv(cache: torch.Tensor, lens: torch.Tensor, rows: torch.Tensor, count
     _req(lens, torch.int32, "lens")
     nseq, L_cap, _ = cache.shape
     _shape(rows, "rows", nseq, None, MLA_DQK)
-    _shape(lens, "lens", nseq); _shape(counts, "counts", nseq)
+    _dims(lens, "lens", nseq)
     if counts is not None:
+        _dims(counts, "counts", nseq)
         _req(counts, torch.int32, "counts")
     if rows.shape[1] == 0:
         return
     with _on(cache, stream, lens, rows, counts, workspace) as s:
         ws = workspace if workspace is not None else nat.alloc_workspace(256, cache.device)
-        _call("misa_append_kv", _p(rows), nseq, rows.shape[1], _p(counts), _p(lens), KV_FORMS[form], _p(cache),
-              _seq_stride(cache), L_cap, _p(ws), ws.numel(), s)
+        _call("misa_append_kv", _ptr(rows), nseq, rows.shape[1], _ptr(counts), _ptr(lens), KV_FORMS[form], _ptr(cache),
+              _seq_stride(cache), L_cap, _ptr(ws), ws.numel(), s)
 
 
 def read_kv(cache: torch.Tensor, seq_of: torch.Tensor, idx: torch.Tensor | None = None,
@@ -122,15 +136,15 @@ def read_kv(cache: torch.Tensor, seq_of: torch.Tensor, idx: torch.Tensor | None 
         raise ValueError("read_kv takes idx or n")
     for name, t in (("first", first), ("prefix_len", prefix_len)):
         if t is not None:
-            _req(t, torch.int32, name); _shape(t, name, T)
+            _req(t, torch.int32, name); _dims(t, name, T)
     if out is not None:
-        _req(out, torch.bfloat16, "out"); _shape(out, "out", T, n, MLA_DQK)
+        _req(out, torch.bfloat16, "out"); _dims(out, "out", T, n, MLA_DQK)
     with _on(cache, stream, seq_of, idx, first, prefix_len, out, workspace) as s:
         if out is None:
             out = torch.empty((T, n, MLA_DQK), dtype=torch.bfloat16, device=cache.device)
         ws = workspace if workspace is not None else nat.alloc_workspace(256, cache.device)
-        _call("misa_read_kv", _p(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _p(seq_of), T, _p(idx),
-              _idx_stride(idx) if idx is not None else 0, _p(first), _p(prefix_len), n, _p(out), _p(ws),
+        _call("misa_read_kv", _ptr(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _ptr(seq_of), T, _ptr(idx),
+              _idx_stride(idx) if idx is not None else 0, _ptr(first), _ptr(prefix_len), n, _ptr(out), _ptr(ws),
               ws.numel(), s)
     return out
 
@@ -147,11 +161,11 @@ def _attend(op: int, q, cache, seq_of, per_query, scale, out, lse, want_lse, wor
     _shape(q, "q", None, None, MLA_DQK)
     T, Hq, _ = q.shape
     nseq, L, _ = cache.shape
-    _shape(seq_of, "seq_of", T)
+    _dims(seq_of, "seq_of", T)
     if out is not None:
-        _req(out, torch.bfloat16, "out"); _shape(out, "out", T, Hq, MLA_DV)
+        _req(out, torch.bfloat16, "out"); _dims(out, "out", T, Hq, MLA_DV)
     if lse is not None:
-        _req(lse, torch.float32, "lse"); _shape(lse, "lse", T, Hq)
+        _req(lse, torch.float32, "lse"); _dims(lse, "lse", T, Hq)
     with _on(q, stream, cache, seq_of, per_query, out, lse, workspace) as s:
         if out is None:
             out = torch.empty((T, Hq, MLA_DV), dtype=torch.bfloat16, device=q.device)
@@ -161,12 +175,12 @@ def _attend(op: int, q, cache, seq_of, per_query, scale, out, lse, want_lse, wor
         if ws is None:
             k = per_query.shape[1] if sparse else 0
             ws = nat.alloc_workspace(nat.workspace_bytes(op, T, Hq, L, 0, k), q.device)
-        head = (_p(q), _p(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _p(seq_of))
-        tail = (float(scale), _p(out), _p(lse), _p(ws), ws.numel(), s)
+        head = (_ptr(q), _ptr(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _ptr(seq_of))
+        tail = (float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s)
         if sparse:
-            _call("misa_sparse_mla_q", *head, T, Hq, _p(per_query), per_query.shape[1], _idx_stride(per_query), *tail)
+            _call("misa_sparse_mla_q", *head, T, Hq, _ptr(per_query), per_query.shape[1], _idx_stride(per_query), *tail)
         else:
-            _call("misa_prefix_mla", *head, _p(per_query), T, Hq, *tail)
+            _call("misa_prefix_mla", *head, _ptr(per_query), T, Hq, *tail)
     return out, lse
 
 
@@ -186,7 +200,7 @@ def prefix_mla(q, cache, seq_of, prefix_len, scale: float, out=None, lse=None, w
     """misa_prefix_mla -> (out [T, Hq, 512] bf16, lse [T, Hq] fp32 or None): q [T,
     Hq, 576] bf16 over the rows below prefix_len [T] int32 of a cache in any form."""
     _req(prefix_len, torch.int32, "prefix_len")
-    _shape(prefix_len, "prefix_len", q.shape[0])
+    _dims(prefix_len, "prefix_len", q.shape[0])
     return _attend(nat.OP_PREFIX_MLA, q, cache, seq_of, prefix_len, scale, out, lse, want_lse, workspace, stream)
 
 
