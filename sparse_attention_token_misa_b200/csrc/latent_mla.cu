@@ -8,44 +8,46 @@
 // more than one SM holds beside the rows.  So a cluster of two CTAs takes a query
 // (or a part of its rows), 64 heads each, and their tensor cores work as a pair
 // (cta_group::2, M = 128): each CTA brings half of the operand that both multiply
-// by, which halves the shared memory reads that bound a 64-head tile otherwise
-// (per 16 of the sum: 32 cycles for 128 heads x 128 rows, 64 for 128 x 256
-// values, the tensor rate; 48 and 80 cycles where one SM reads both operands).
+// by, which halves the shared memory reads that bound a 64-head tile otherwise.
 //
-// Rows come in tiles of 128.  Per tile:
-//  1. CTA u brings rows [64 u, 64 u + 64) of the tile to shared memory as bf16, in 9
+// Rows come in tiles of 64.  Per tile:
+//  1. CTA u brings rows [32 u, 32 u + 32) of the tile to shared memory as bf16, in 9
 //     blocks of 64 entries: quantised rows widened (exactly) in registers, bf16 rows
 //     by TMA.  S = Q K^T reads these blocks.  S in TMEM: lane l < 64 has head l
-//     against rows 0..63, lane 64 + l the same head against rows 64..127.
+//     against rows 0..31, lane 64 + l the same head against rows 32..63.
 //  2. Softmax in one pass with a running reference m: when a tile's maximum is
 //     more than 2^8 above 2^m, the sums so far are scaled and m moves (p stays
 //     below 2^8, exact enough in bf16 and fp32).  p goes to shared memory as bf16.
-//  3. O += P V needs entries [256 u, 256 u + 256) of all 128 rows in CTA u: eight
-//     warps of each CTA copy the blocks it brought to the CTA that multiplies them,
-//     through registers (rows of 64 entries in 128-byte swizzled atoms serve both
+//  3. O += P V needs entries [256 u, 256 u + 256) of all 64 rows in CTA u: eight
+//     warps of each CTA write the blocks it brought to the CTA that multiplies them,
+//     from registers (rows of 64 entries in 128-byte swizzled atoms serve both
 //     products, K-major in one and MN-major in the other).  So a row is read from L2
 //     and widened once.  O stays in TMEM, 256 columns.
-// S has four places, so that the products run ahead: a tile's way through softmax
-// and back takes about 2900 cycles (with two places the speed was half of that).
+// Every operand has two stages and S four places: a tile's way from its rows through
+// the softmax to O takes about 6000 cycles, three times its share of the tensor cores
+// (with one stage of 128 rows, or S held back until the O before it, the latency of
+// that way was the speed: mx8 3.4 us for 128 rows).
 //
-// What bounds a tile of bf16 rows is 74 KB a CTA from L2 (about 30 bytes a cycle:
-// 2500 cycles, and all rows twice would be 139 KB) and 32 KB to the other CTA (16
-// bytes a cycle: 2000), of quantised rows the widening as well; the products take
-// 2176 cycles of the tensor cores, the softmax 1500 of its warps.
+// What bounds a tile is shared memory, which both products read at its full rate:
+// S 36 x 24 cycles (queries and rows, 3 KB at 128 bytes a cycle), O 4 x 2 x 48, and
+// rows and values written (bf16: and copied) once more, about 2000 cycles in all.
+// Measured, 74 queries of one cache, for 128 rows of it: bf16 2.1 us (1.26 PFLOP/s,
+// 0.79 of cuBLAS's measured rate), mx8 2.5, mx4 2.4, where the eight warps that widen
+// rows take longer than that.  More of them were slower (16: mx8 2.9), and so were
+// spilled registers: shared memory leaves L1 little room for a stack.
 //
 // A cluster stays on its SMs and takes one item in 74 (a query, or a part of its
 // rows), each role on its own: the rows of the next item come while the output of
 // this one leaves.  (A cluster an item spent 9 us on starting, queries and output
-// around 3 us a tile.)  Few queries: the rows of each are split over several
-// items, whose partial sums a second kernel joins in a fixed order.
+// around 3 us a tile; now an item costs 4.)  Few queries: the rows of each are split
+// over several items, whose partial sums a second kernel joins in a fixed order.
 //
 // Roles (640 threads a CTA): two warpgroups softmax and output, eight warps that bring
 // quantised rows or copy bf16 ones, one warp that has TMEM and, in the first CTA,
-// issues the MMAs, and three that ask for what comes by TMA and pass on what has
-// landed.  Shared memory is addressed from one 32-bit base: with a pointer a barrier
-// the kernel spilled, and what shared memory leaves of L1 does not hold the stack.
-// Code is kept small (loops, not copies): at 140 KB the instruction caches, which
-// many SMs share, halved the speed.  Waits are bounded.
+// issues S, one that issues O, and two that ask for what comes by TMA and pass on what
+// has landed.  Shared memory is addressed from one 32-bit base: with a pointer a
+// barrier the kernel spilled.  Code is kept small (loops, not copies): at 140 KB the
+// instruction caches, which many SMs share, halved the speed.  Waits are bounded.
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"
@@ -85,14 +87,14 @@ constexpr uint32_t kOEmpty = kPvDone + 16;        // (one) first CTA: O of the i
 constexpr uint32_t kQFull = kOEmpty + 8;          // (one) this CTA's queries landed
 constexpr uint32_t kQReady = kQFull + 8;          // (one) first CTA: queries landed (bf16: the other CTA's)
 constexpr uint32_t kQEmpty = kQReady + 8;         // (one) the item's last S complete
-constexpr uint32_t kDone = kQEmpty + 8;           // (one) every MMA retired
+constexpr uint32_t kDone = kQEmpty + 8;           // (one) every MMA of both warps that issue them retired
 constexpr uint32_t kOffTmem = kDone + 8;
 constexpr uint32_t kOffMax = (kOffTmem + 8 + 15) / 16 * 16;   // [2][128] floats: a tile's maxima, by softmax warpgroup
 constexpr uint32_t kOffRef = kOffMax + 1024;      // [2][64]: a head's reference m after a tile
 constexpr uint32_t kOffSum = kOffRef + 512;       // [2][128]: an item's sums of the warpgroup that does not finish it
 constexpr int kSmemBytes = kOffSum + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-// Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-20 the rest.
+// Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-19 the rest.
 constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps;
 constexpr int kThreads = (kMmaWarp + 4) * 32;
 constexpr uint32_t kTmemS = 256;                  // O: columns 0..255, S: four places of 32 columns
@@ -132,16 +134,7 @@ __device__ __forceinline__ void st_async16(uint32_t remote, uint4 v, uint32_t re
                "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(remote_bar)
                : "memory");
 }
-// Whether the phase of `parity` is over (try: may sleep a while first).
-__device__ __forceinline__ uint32_t test_phase(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok;
-}
+// Whether the phase of `parity` is over (may sleep a while first).
 __device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -520,7 +513,7 @@ __device__ __forceinline__ void load_queries(const MlaParams& p, uint32_t rank, 
   for (int b = 0; b < kBlocks; ++b)
     tma_2d(sb + kOffQ + b * kQBlock, q_map, sb + kQFull, b * 64, t * p.a.Hq + static_cast<int>(rank) * kHeads);
 }
-constexpr int kAhead = 4;   // tiles
+constexpr int kAhead = 4;   // tiles (2, 8 and 12: the same within 3 %)
 template <int kFmt>
 __device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, int lane, const CUtensorMap* q_map, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
