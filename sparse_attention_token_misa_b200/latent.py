@@ -37,9 +37,10 @@ def alloc_kv_cache(nseq: int, L: int, form: str, device=None) -> torch.Tensor:
 
 
 def _cache_form(cache: torch.Tensor) -> str:
-    form = _FORM_OF.get((cache.dtype, cache.shape[2])) if cache.dim() == 3 else None
+    shape = cache.shape
+    form = _FORM_OF.get((cache.dtype, shape[2])) if len(shape) == 3 else None
     if form is not None:
-        if cache.stride(2) != 1 or cache.stride(1) != cache.shape[2]:
+        if cache.stride()[1:] != (shape[2], 1):
             raise ValueError("cache rows must be contiguous and follow one another")
         return form
     raise ValueError("cache: expected shape [nseq, L, 576] bf16 or [nseq, L, 656 or 400] uint8, got "
@@ -141,7 +142,7 @@ def read_kv(cache: torch.Tensor, seq_of: torch.Tensor, idx: torch.Tensor | None 
         _req(out, torch.bfloat16, "out"); _dims(out, "out", T, n, MLA_DQK)
     with _on(cache, stream, seq_of, idx, first, prefix_len, out, workspace) as s:
         if out is None:
-            out = torch.empty((T, n, MLA_DQK), dtype=torch.bfloat16, device=cache.device)
+            out = cache.new_empty((T, n, MLA_DQK), dtype=torch.bfloat16)
         ws = workspace if workspace is not None else nat.alloc_workspace(256, cache.device)
         _call("misa_read_kv", _ptr(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _ptr(seq_of), T, _ptr(idx),
               _idx_stride(idx) if idx is not None else 0, _ptr(first), _ptr(prefix_len), n, _ptr(out), _ptr(ws),
@@ -168,9 +169,9 @@ def _attend(op: int, q, cache, seq_of, per_query, scale, out, lse, want_lse, wor
         _req(lse, torch.float32, "lse"); _dims(lse, "lse", T, Hq)
     with _on(q, stream, cache, seq_of, per_query, out, lse, workspace) as s:
         if out is None:
-            out = torch.empty((T, Hq, MLA_DV), dtype=torch.bfloat16, device=q.device)
+            out = q.new_empty((T, Hq, MLA_DV))
         if lse is None and want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((T, Hq), dtype=torch.float32)
         ws = workspace
         if ws is None:
             k = per_query.shape[1] if sparse else 0
