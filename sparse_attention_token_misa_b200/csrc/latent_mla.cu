@@ -51,6 +51,7 @@
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"
+#include "softmax_exchange.h"
 
 namespace misa {
 
@@ -89,10 +90,8 @@ constexpr uint32_t kQReady = kQFull + 8;          // (one) first CTA: queries la
 constexpr uint32_t kQEmpty = kQReady + 8;         // (one) the item's last S complete
 constexpr uint32_t kDone = kQEmpty + 8;           // (one) every MMA of both warps that issue them retired
 constexpr uint32_t kOffTmem = kDone + 8;
-constexpr uint32_t kOffMax = (kOffTmem + 8 + 15) / 16 * 16;   // [2][128] floats: a tile's maxima, by softmax warpgroup
-constexpr uint32_t kOffRef = kOffMax + 1024;      // [2][64]: a head's reference m after a tile
-constexpr uint32_t kOffSum = kOffRef + 512;       // [2][128]: an item's sums of the warpgroup that does not finish it
-constexpr int kSmemBytes = kOffSum + 1024;
+constexpr uint32_t kOffExchange = (kOffTmem + 8 + 15) / 16 * 16;   // maxima, references, sums (softmax_exchange.h)
+constexpr int kSmemBytes = kOffExchange + kExBytes;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Warps: 0-7 softmax and output, 8-15 bring quantised rows or copy bf16 ones, 16-19 the rest.
 constexpr int kRowWarp0 = 8, kRowWarps = 8, kMmaWarp = kRowWarp0 + kRowWarps;
@@ -669,12 +668,17 @@ done:
   __syncwarp();
 }
 
-// Named barriers: the maxima of a tile (128 threads, by warpgroup), the reference
-// after a tile (256, by the tile's number), an item's sums (256, by the item's).
-constexpr int kBarMax = 1, kBarRef = 3, kBarSum = 5;
 __device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The softmax warpgroups' exchange area and its barriers.
+struct ExchangeIo {
+  uint32_t base;
+  __device__ __forceinline__ void store(uint32_t at, uint32_t v) const { st_shared(base + at, v); }
+  __device__ __forceinline__ uint32_t load(uint32_t at) const { return ld_shared(base + at); }
+  __device__ __forceinline__ void sync(int id, int nthreads) const { named_bar_sync(id, nthreads); }
+  __device__ __forceinline__ void arrive(int id, int nthreads) const { named_bar_arrive(id, nthreads); }
+};
 
 // Softmax and output, two warpgroups: each takes every other tile, so that one's
 // loads, barriers and fences pass while the other one counts; between them goes the
@@ -692,6 +696,7 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
   const float kNegInf = -__int_as_float(0x7f800000);
   const float c = fmaxf(a.scale_log2, 1.2e-38f);   // a scale of 0 weighs all rows alike; -inf stays -inf
   const uint32_t my_p = sb + kOffP + group * kPStage;
+  SoftmaxExchange<ExchangeIo> exchange = {{sb + kOffExchange}, group, tid};
   bool ok = true;
   Turn n;
   uint32_t items = 0;                              // that have rows, so far
@@ -749,19 +754,12 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
       }
       here = row_at(n.n + 2);
       // the other half of the tile's rows for the same head
-      st_shared(sb + kOffMax + group * 512 + tid * 4, __float_as_uint(mx));
-      named_bar_sync(kBarMax + group, 128);
-      mx = fmaxf(mx, __uint_as_float(ld_shared(sb + kOffMax + group * 512 + (tid ^ 64) * 4))) * c;
+      mx = fmaxf(mx, __uint_as_float(exchange.other_half(__float_as_uint(mx)))) * c;
       // the reference after the tile before, moved if this tile is far above it
-      m_prev = kNegInf;
-      if (n.n > 0) {
-        named_bar_sync(kBarRef + (group ^ 1u), 256);
-        if (n.n > first) m_prev = __uint_as_float(ld_shared(sb + kOffRef + (group ^ 1u) * 256 + hl * 4));
-      }
+      m_prev = __uint_as_float(exchange.reference_before(n.n, first, 0xff800000u));
       const bool moved = mx > m_prev + 8.f || (m_prev == kNegInf && mx > kNegInf);
       const float m_new = moved ? mx : m_prev;
-      if (half == 0) st_shared(sb + kOffRef + group * 256 + hl * 4, __float_as_uint(m_new));
-      named_bar_arrive(kBarRef + group, 256);
+      exchange.set_reference(__float_as_uint(m_new));
       if (m_new != m) {
         l *= m == kNegInf ? 0.f : ex2(m - m_new);
         m = m_new;
@@ -807,20 +805,14 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
     const uint32_t turn = items & 1;
     ++items;
     if (((end - 1) & 1) != group) {   // the other warpgroup finishes the item
-      st_shared(sb + kOffSum + turn * 512 + tid * 4, __float_as_uint(l));
-      named_bar_arrive(kBarSum + turn, 256);
+      exchange.hand_over(turn, __float_as_uint(l));
       continue;
     }
     // The sums of both warpgroups and both halves: the other warpgroup's are relative
     // to the reference before the last tile.
-    named_bar_sync(kBarMax + group, 128);   // the last tile's maxima have been read
-    st_shared(sb + kOffMax + group * 512 + tid * 4, __float_as_uint(l));
-    named_bar_sync(kBarSum + turn, 256);
-    l += __uint_as_float(ld_shared(sb + kOffMax + group * 512 + (tid ^ 64) * 4));
-    named_bar_sync(kBarMax + group, 128);   // and so have these
+    l += __uint_as_float(exchange.other_half_sum(turn, __float_as_uint(l)));
     if (ntiles > 1) {
-      const float other = __uint_as_float(ld_shared(sb + kOffSum + turn * 512 + tid * 4)) +
-                          __uint_as_float(ld_shared(sb + kOffSum + turn * 512 + (tid ^ 64) * 4));
+      const float other = __uint_as_float(exchange.handed_over(turn, 0)) + __uint_as_float(exchange.handed_over(turn, 1));
       l += other * (m_prev == m ? 1.f : m_prev == kNegInf ? 0.f : ex2(m_prev - m));
     }
     Turn last;

@@ -1,0 +1,39 @@
+"""The softmax of the latent attention where its parts differ most: the two halves of
+a tile's rows, one tile and the next.  Tolerances as in test_gpu_latent_mla.py."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sparse_attention_token_misa_b200 as misa
+from test_gpu_latent_mla import FORMS, SCALE, _check, _i32, _prefix_idx
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,L", [(160, 64 * 5 + 7), (80, 64 * 2), (3, 64 * 40)])
+def test_halves_and_tiles_of_different_size(form, T, L):
+    """Every half tile (32 rows) has its own size of score, some 20 apart, so that a
+    maximum taken from another tile or half would be far off: in a cluster's first
+    tiles, in several items a cluster, in items of several lengths.  The same bits
+    every time."""
+    g = torch.Generator().manual_seed(T)
+    q = torch.randn(T, 128, 576, generator=g) * 0.5
+    q[:, :, 512:] = 1.0
+    rows = torch.randn(1, L, 576, generator=g) * 0.3
+    size = torch.tensor([20.0, -20.0, -20.0, 0.0, -20.0, 20.0, 0.0, 7.0])
+    rows[0, :, 512:] += (size[torch.arange(L) // 32 % 8] / (64 * SCALE))[:, None]
+    q, rows = q.bfloat16(), rows.bfloat16()
+    cache = misa.alloc_kv_cache(1, L, form)
+    misa.append_kv(cache, _i32([0]), rows.cuda())
+    held = oracle.latent_values(rows.double().numpy(), form)
+    lens = [L - (37 * t) % L for t in range(T)]
+    args = (q.cuda(), cache, _i32([0] * T), _i32(lens), SCALE)
+    ws = misa.alloc_workspace(misa.workspace_bytes(misa.OP_PREFIX_MLA, T, 128, L, 0))
+    out, lse = misa.prefix_mla(*args, want_lse=True, workspace=ws)
+    assert misa.error_query(ws) == 0
+    _check(out, lse, q, held, np.zeros(T, np.int64), _prefix_idx(lens, L), SCALE)
+    for _ in range(20):
+        again, lse2 = misa.prefix_mla(*args, want_lse=True, workspace=ws)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
