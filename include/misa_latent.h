@@ -42,7 +42,10 @@ extern "C" {
 
 /* Operation ids for misa_workspace_bytes (arguments it uses):
  *   APPEND_KV: none;  READ_KV: none;  SPARSE_MLA_Q: T, H (= Hq), k;
- *   PREFIX_MLA: T, H (= Hq), L. */
+ *   PREFIX_MLA: T, H (= Hq), L.
+ * A workspace of that size also serves every call with fewer of any of them.  It
+ * is 256 bytes and 2056 Hq bytes for each partial result: at most 128 a query, one
+ * for each 64 rows, 296 in all.  Only the error word has to be cleared, once. */
 #define MISA_OP_APPEND_KV 9
 #define MISA_OP_READ_KV 10
 #define MISA_OP_SPARSE_MLA_Q 11

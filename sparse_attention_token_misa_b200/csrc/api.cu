@@ -133,9 +133,9 @@ size_t misa_workspace_bytes(int op, int T, int H, int64_t L, int B, int k, int k
       return kErrBytes;
     case MISA_OP_SPARSE_MLA_Q:
       if (k < 1) return 0;
-      return kErrBytes + misa::latent_mla_scratch_bytes(T, H, k);
+      return kErrBytes + misa::latent_mla_scratch_bound(T, H, k);
     case MISA_OP_PREFIX_MLA:
-      return kErrBytes + misa::latent_mla_scratch_bytes(T, H, L);
+      return kErrBytes + misa::latent_mla_scratch_bound(T, H, L);
     case MISA_OP_HISA_BLOCK_FILTER: {
       if (B < 1) return 0;
       const int64_t M = ceil_div(L, B);

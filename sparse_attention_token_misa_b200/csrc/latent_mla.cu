@@ -48,6 +48,8 @@
 // has landed.  Shared memory is addressed from one 32-bit base: with a pointer a
 // barrier the kernel spilled.  Code is kept small (loops, not copies): at 140 KB the
 // instruction caches, which many SMs share, halved the speed.  Waits are bounded.
+#include <algorithm>
+
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"
@@ -1054,12 +1056,14 @@ constexpr int kSlots = 74;
 // 2048 mx8 rows 51 us whole and 69 in halves, 32 queries 49 and 40; 16 of 32,768 rows
 // 177 us in four parts and 187 in nine.
 constexpr int kItemTiles = 16, kJoinTiles = 6;
+constexpr int kMaxParts = 4 * kSlots;   // of all queries together
+int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 int pick_splits(int T, int64_t n) {
-  const int64_t tiles = (n + kTile - 1) / kTile;
+  const int64_t tiles = tiles_of(n);
   int best = 1;
   int64_t best_cost = -1;
   for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
-    if (s > 1 && static_cast<int64_t>(T) * s > 4 * kSlots) break;
+    if (s > 1 && static_cast<int64_t>(T) * s > kMaxParts) break;
     const int64_t rounds = (static_cast<int64_t>(T) * s + kSlots - 1) / kSlots;
     const int64_t cost = rounds * ((tiles + s - 1) / s + kItemTiles) + (s > 1 ? kJoinTiles : 0);
     if (best_cost < 0 || cost < best_cost) {
@@ -1069,12 +1073,25 @@ int pick_splits(int T, int64_t n) {
   }
   return best;
 }
+size_t part_bytes(int64_t parts, int Hq) { return static_cast<size_t>(parts) * Hq * (kDv + 2) * sizeof(float); }
 
 }  // namespace
 
 size_t latent_mla_scratch_bytes(int T, int Hq, int64_t n) {
   const int s = pick_splits(T, n);
-  return s > 1 ? static_cast<size_t>(T) * s * Hq * (kDv + 2) * sizeof(float) : 0;
+  return s > 1 ? part_bytes(static_cast<int64_t>(T) * s, Hq) : 0;
+}
+
+// Fewer queries or rows may be split into more parts than many (2048 rows: 32 queries
+// into 64 parts, 64 queries not at all), so the bound goes over all T' <= T; for each
+// it takes what pick_splits may choose at most, which does not fall with n.
+size_t latent_mla_scratch_bound(int T, int Hq, int64_t n) {
+  int64_t most = 0;
+  for (int t = 1; t <= T && 2 * t <= kMaxParts; ++t) {
+    const int64_t s = std::min({static_cast<int64_t>(kMaxSplits), tiles_of(n), static_cast<int64_t>(kMaxParts / t)});
+    if (s > 1) most = std::max(most, t * s);
+  }
+  return part_bytes(most, Hq);
 }
 
 cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream) {

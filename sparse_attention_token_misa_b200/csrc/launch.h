@@ -142,8 +142,10 @@ struct LatentArgs {
   uint32_t* err;
   void* scratch;
 };
-// Scratch behind the error word for T queries of Hq heads with at most n rows each.
+// Scratch behind the error word for T queries of Hq heads with at most n rows each:
+// what that call uses, and what it and every call with fewer of any of them uses at most.
 size_t latent_mla_scratch_bytes(int T, int Hq, int64_t n);
+size_t latent_mla_scratch_bound(int T, int Hq, int64_t n);
 cudaError_t launch_latent_mla(const LatentArgs& a, cudaStream_t stream);
 
 cudaError_t launch_hisa_expand(const int32_t* blocks, const int32_t* prefix_len, int T, int m, int B, int S,

@@ -175,7 +175,8 @@ def _attend(op: int, q, cache, seq_of, per_query, scale, out, lse, want_lse, wor
         ws = workspace
         if ws is None:
             k = per_query.shape[1] if sparse else 0
-            ws = nat.alloc_workspace(nat.workspace_bytes(op, T, Hq, L, 0, k), q.device)
+            ws = torch.empty(nat.workspace_bytes(op, T, Hq, L, 0, k), dtype=torch.uint8, device=q.device)
+            ws[:256].zero_()   # the error word; partial results are written before they are read
         head = (_ptr(q), _ptr(cache), KV_FORMS[form], nseq, _seq_stride(cache), L, _ptr(seq_of))
         tail = (float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s)
         if sparse:

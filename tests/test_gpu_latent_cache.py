@@ -1,0 +1,43 @@
+"""Workspaces, buffers and lengths that a program keeps between calls of the latent
+attention: used for other sizes, with old contents, one call after the other."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sparse_attention_token_misa_b200 as misa
+from test_gpu_latent_mla import FORMS, SCALE, _check, _draw_idx, _i32, _prefix_idx, _setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_workspace_of_a_larger_batch(form):
+    """One workspace, sized for the largest batch and never cleared behind its error
+    word, serves smaller ones, whose rows are split into more parts; so do calls that
+    bring none."""
+    L, Hq = 2048, 64
+    q, cache, held = _setup(40, 2, L, form, 70, Hq)
+    ws = misa.alloc_workspace(misa.workspace_bytes(misa.OP_PREFIX_MLA, 70, Hq, L, 0))
+    for T in (70, 32, 3, 1):
+        ws[256:].fill_(0xFF)
+        seq, lens = np.arange(T) % 2, [L - 5 * t for t in range(T)]
+        args = (q[:T].cuda(), cache, _i32(seq), _i32(lens), SCALE)
+        out, lse = misa.prefix_mla(*args, want_lse=True, workspace=ws)
+        assert misa.error_query(ws) == 0
+        alone, lse_alone = misa.prefix_mla(*args, want_lse=True)
+        assert torch.equal(out, alone) and torch.equal(lse, lse_alone)
+        _check(out, lse, q[:T], held, seq, _prefix_idx(lens, L), SCALE)
+
+
+@pytest.mark.parametrize("form", ["mx8", "mx4"])
+def test_shorter_lists_in_the_workspace_of_longer_ones(form):
+    L, k = 6000, 4737
+    q, cache, held = _setup(41, 1, L, form, 1, 128)
+    ws = misa.alloc_workspace(misa.workspace_bytes(misa.OP_SPARSE_MLA_Q, 1, 128, L, 0, k))
+    for n in (4737, 4736, 2048, 1):
+        ws[256:].fill_(0xFF)
+        idx = _draw_idx(n, 1, L, n, 0)
+        out, lse = misa.sparse_mla_q(q.cuda(), cache, _i32([0]), _i32(idx), SCALE, want_lse=True, workspace=ws)
+        assert misa.error_query(ws) == 0
+        _check(out, lse, q, held, np.array([0]), idx, SCALE)
