@@ -209,14 +209,18 @@ def prefix_mla(q, cache, seq_of, prefix_len, scale: float, out=None, lse=None, w
 class LatentCache:
     """The latent caches of nseq sequences with their lengths, and the buffers of
     one batch of T queries: append and attend allocate nothing and can be
-    captured in a CUDA graph (lens advances on the device)."""
+    captured in a CUDA graph (lens advances on the device).
+
+    attend and attend_prefix have outputs of their own, which the next call of the
+    same one overwrites; out and lse are those of the last call of either."""
 
     def __init__(self, nseq: int, L: int, form: str, T: int, Hq: int, k: int, device="cuda"):
         self.nseq, self.L, self.form, self.T, self.Hq, self.k = nseq, L, form, T, Hq, k
         self.rows = alloc_kv_cache(nseq, L, form, device)
         self.lens = torch.zeros(nseq, dtype=torch.int32, device=device)
-        self.out = torch.empty((T, Hq, MLA_DV), dtype=torch.bfloat16, device=device)
-        self.lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+        self._listed, self._prefix = ((torch.empty((T, Hq, MLA_DV), dtype=torch.bfloat16, device=device),
+                                       torch.empty((T, Hq), dtype=torch.float32, device=device)) for _ in range(2))
+        self.out, self.lse = self._listed
         self.ws = nat.alloc_workspace(256, device)
         op = nat.OP_SPARSE_MLA if form == "bf16" else nat.OP_SPARSE_MLA_Q
         self.ws_sparse = nat.alloc_workspace(nat.workspace_bytes(op, T, Hq, L, 0, k), device)
@@ -234,6 +238,7 @@ class LatentCache:
 
     def attend(self, q, seq_of, idx, scale: float):
         """Over the tokens the indexer lists -> (out, lse)."""
+        self.out, self.lse = self._listed
         if self.form == "bf16":
             return nat.sparse_mla(q, self.rows, seq_of, idx, scale, out=self.out, lse=self.lse,
                                   workspace=self.ws_sparse)
@@ -241,5 +246,6 @@ class LatentCache:
 
     def attend_prefix(self, q, seq_of, prefix_len, scale: float):
         """Over the whole prefix -> (out, lse)."""
+        self.out, self.lse = self._prefix
         return prefix_mla(q, self.rows, seq_of, prefix_len, scale, out=self.out, lse=self.lse,
                           workspace=self.ws_prefix)

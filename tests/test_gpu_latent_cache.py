@@ -41,3 +41,21 @@ def test_shorter_lists_in_the_workspace_of_longer_ones(form):
         out, lse = misa.sparse_mla_q(q.cuda(), cache, _i32([0]), _i32(idx), SCALE, want_lse=True, workspace=ws)
         assert misa.error_query(ws) == 0
         _check(out, lse, q, held, np.array([0]), idx, SCALE)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_listed_and_prefix_side_by_side(form):
+    """Both attentions of a step, compared behind it: each with its own oracle value."""
+    T, L, k, Hq = 3, 500, 200, 128
+    g = torch.Generator().manual_seed(42)
+    rows, q = torch.randn(T, L, 576, generator=g).bfloat16(), torch.randn(T, Hq, 576, generator=g).bfloat16()
+    held = oracle.latent_values(rows.double().numpy(), form)
+    lc = misa.LatentCache(T, L, form, T, Hq, k)
+    lc.append(rows.cuda())
+    idx, seq = _draw_idx(42, T, L, k, 20), _i32(range(T))
+    listed = lc.attend(q.cuda(), seq, _i32(idx), SCALE)
+    prefix = lc.attend_prefix(q.cuda(), seq, lc.lens, SCALE)
+    # the bf16 form of the listed tokens rounds its weights before their sum too
+    more = dict(roundings=3, lse_more=1.01 * 2.0 ** -8) if form == "bf16" else {}
+    _check(*listed, q, held, np.arange(T), idx, SCALE, **more)
+    _check(*prefix, q, held, np.arange(T), _prefix_idx([L] * T, L), SCALE)

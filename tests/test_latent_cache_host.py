@@ -1,0 +1,50 @@
+"""LatentCache on the host: what it passes to the library's calls, which are replaced
+by stand-ins, and what it keeps between them."""
+import pytest
+import torch
+
+import sparse_attention_token_misa_b200 as misa
+from sparse_attention_token_misa_b200 import _native as nat
+from sparse_attention_token_misa_b200 import latent
+
+bf, i32 = torch.bfloat16, torch.int32
+FORMS = ["bf16", "mx8", "mx4"]
+
+
+def cache(form, nseq=2, L=16, T=2, Hq=4, k=8):
+    return misa.LatentCache(nseq, L, form, T, Hq, k, device="cpu")
+
+
+def attention(value):
+    """Stands for an attention call: fills the outputs it is given."""
+    def call(q, rows, seq_of, per_query, scale, out, lse, workspace):
+        out.fill_(value); lse.fill_(value)
+        return out, lse
+    return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    monkeypatch.setattr(nat, "sparse_mla", attention(1.0))
+    monkeypatch.setattr(latent, "sparse_mla_q", attention(1.0))
+    monkeypatch.setattr(latent, "prefix_mla", attention(2.0))
+
+
+QUERY = (torch.zeros(2, 4, 576, dtype=bf), torch.zeros(2, dtype=i32))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("listed_first", [True, False])
+def test_the_two_results_stand_side_by_side(calls, form, listed_first):
+    """The comparison of the listed tokens with the whole prefix: neither call's
+    result is the other's.  `out` and `lse` are the last call's."""
+    lc = cache(form)
+    for name in ("attend", "attend_prefix") if listed_first else ("attend_prefix", "attend"):
+        r = getattr(lc, name)(*QUERY, torch.zeros(2, 8, dtype=i32) if name == "attend" else QUERY[1], 0.1)
+        assert lc.out is r[0] and lc.lse is r[1]
+        if name == "attend":
+            listed = r
+        else:
+            prefix = r
+    for a, b in zip(listed, prefix):
+        assert (a == 1).all() and (b == 2).all()
