@@ -696,7 +696,12 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
   const int h0 = static_cast<int>(rank) * kHeads + (warp & 1) * 32;   // first head of the warp
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
   const float kNegInf = -__int_as_float(0x7f800000);
-  const float c = fmaxf(a.scale_log2, 1.2e-38f);   // a scale of 0 weighs all rows alike; -inf stays -inf
+  // A scale of 0 takes the scores away first (a NaN or an infinity becomes NaN, as in
+  // 0 * s) and then weighs by 1, so that -inf times the scale stays -inf for the rows
+  // that are not there.  (With the smallest normal number in place of 0, scores of 1e37
+  // still weighed rows apart.)
+  const bool flat = a.scale_log2 == 0.f;
+  const float c = flat ? 1.f : a.scale_log2;
   const uint32_t my_p = sb + kOffP + group * kPStage;
   SoftmaxExchange<ExchangeIo> exchange = {{sb + kOffExchange}, group, tid};
   bool ok = true;
@@ -744,6 +749,10 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_in(sb + kSEmpty + n.at4(), 0);
+        if (__builtin_expect(flat, 0)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * 0.f);
+        }
         if (live != 0xffffffffu) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
