@@ -240,8 +240,9 @@ class LatentCache:
         """Over the tokens the indexer lists -> (out, lse)."""
         self.out, self.lse = self._listed
         if self.form == "bf16":
-            return nat.sparse_mla(q, self.rows, seq_of, idx, scale, out=self.out, lse=self.lse,
-                                  workspace=self.ws_sparse)
+            with _on(self.rows, None, q, seq_of, idx, self.out, self.lse, self.ws_sparse) as s:
+                return nat.sparse_mla(q, self.rows, seq_of, idx, scale, out=self.out, lse=self.lse,
+                                      workspace=self.ws_sparse, stream=s)
         return sparse_mla_q(q, self.rows, seq_of, idx, scale, out=self.out, lse=self.lse, workspace=self.ws_sparse)
 
     def attend_prefix(self, q, seq_of, prefix_len, scale: float):

@@ -1,5 +1,7 @@
 """LatentCache on the host: what it passes to the library's calls, which are replaced
 by stand-ins, and what it keeps between them."""
+import contextlib
+
 import pytest
 import torch
 
@@ -17,7 +19,7 @@ def cache(form, nseq=2, L=16, T=2, Hq=4, k=8):
 
 def attention(value):
     """Stands for an attention call: fills the outputs it is given."""
-    def call(q, rows, seq_of, per_query, scale, out, lse, workspace):
+    def call(q, rows, seq_of, per_query, scale, out, lse, workspace, stream=None):
         out.fill_(value); lse.fill_(value)
         return out, lse
     return call
@@ -28,6 +30,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(nat, "sparse_mla", attention(1.0))
     monkeypatch.setattr(latent, "sparse_mla_q", attention(1.0))
     monkeypatch.setattr(latent, "prefix_mla", attention(2.0))
+    monkeypatch.setattr(latent, "_on", lambda first, stream, *others: contextlib.nullcontext(0))
 
 
 QUERY = (torch.zeros(2, 4, 576, dtype=bf), torch.zeros(2, dtype=i32))
@@ -48,3 +51,25 @@ def test_the_two_results_stand_side_by_side(calls, form, listed_first):
             prefix = r
     for a, b in zip(listed, prefix):
         assert (a == 1).all() and (b == 2).all()
+
+
+def test_bf16_attention_runs_on_the_tensors_device(calls, monkeypatch):
+    """sparse_mla launches on the current device: attend makes the cache's device the
+    current one around it, and refuses tensors of another, as the other calls do."""
+    lc, idx, made = cache("bf16"), torch.zeros(2, 8, dtype=i32), []
+
+    @contextlib.contextmanager
+    def on(first, stream, *others):
+        made.append((stream, {first.data_ptr(), *(t.data_ptr() for t in others)}))
+        yield 77
+        made.append("left")
+
+    def sparse_mla(q, rows, seq_of, idx, scale, out, lse, workspace, stream):
+        assert len(made) == 1 and stream == 77
+        return out, lse
+
+    monkeypatch.setattr(latent, "_on", on)
+    monkeypatch.setattr(nat, "sparse_mla", sparse_mla)
+    out, lse = lc.attend(*QUERY, idx, 0.1)
+    used = {t.data_ptr() for t in (*QUERY, lc.rows, idx, out, lse, lc.ws_sparse)}
+    assert made == [(None, used), "left"]
