@@ -228,12 +228,15 @@ class LatentCache:
 
     def append(self, rows: torch.Tensor, counts: torch.Tensor | None = None) -> None:
         """Write new rows behind each sequence's last one and advance its length.  A
-        sequence whose rows no longer fit (or whose count is out of range) is left
-        as it was, as misa_append_kv skips it and records it in `ws`."""
+        sequence whose rows no longer fit (or whose count or length is out of range)
+        is left as it was, as misa_append_kv skips it and records it in `ws`."""
         append_kv(self.rows, self.lens, rows, counts=counts, workspace=self.ws)
         n = rows.shape[1]
-        new = self.lens + (n if counts is None else counts)
-        fits = (new <= self.L) if counts is None else (new <= self.L) & (counts >= 0) & (counts <= n)
+        more = n if counts is None else counts
+        new = self.lens + more
+        fits = (new <= self.L) & (new >= more)   # (a length below zero, or past 2^31, gives less)
+        if counts is not None:
+            fits &= (counts >= 0) & (counts <= n)
         self.lens.copy_(torch.where(fits, new, self.lens))
 
     def attend(self, q, seq_of, idx, scale: float):

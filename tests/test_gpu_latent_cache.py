@@ -59,3 +59,26 @@ def test_listed_and_prefix_side_by_side(form):
     more = dict(roundings=3, lse_more=1.01 * 2.0 ** -8) if form == "bf16" else {}
     _check(*listed, q, held, np.arange(T), idx, SCALE, **more)
     _check(*prefix, q, held, np.arange(T), _prefix_idx([L] * T, L), SCALE)
+
+
+@pytest.mark.parametrize("counted", [False, True])
+def test_lengths_and_rows_advance_together(counted):
+    """Where append moves a length it has written the rows, and nowhere else."""
+    L, n = 16, 3
+    lens = [-1, 0, 5, 13, 14, 16, 17, 2 ** 31 - 1, -2 ** 31]
+    counts = [3, 0, 2, 3, 2, 1, 0, 3, 3] if counted else [n] * len(lens)
+    rows = torch.randn(len(lens), n, 576, generator=torch.Generator().manual_seed(43)).bfloat16()
+    lc = misa.LatentCache(len(lens), L, "mx8", T=1, Hq=1, k=1)
+    lc.rows.fill_(0x5A)
+    lc.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    want = lc.rows.cpu()
+    held = torch.from_numpy(oracle.latent_bytes(rows.double().numpy(), "mx8"))
+    new = []
+    for b, (l, c) in enumerate(zip(lens, counts)):
+        fits = 0 <= c <= n and l >= 0 and l + c <= L
+        if fits:
+            want[b, l:l + c] = held[b, :c]
+        new.append(l + c if fits else l)
+    lc.append(rows.cuda(), counts=_i32(counts) if counted else None)
+    assert lc.lens.tolist() == new and torch.equal(lc.rows.cpu(), want)
+    assert misa.error_query(lc.ws) == misa._native.DEVERR_BAD_LEN

@@ -73,3 +73,26 @@ def test_bf16_attention_runs_on_the_tensors_device(calls, monkeypatch):
     out, lse = lc.attend(*QUERY, idx, 0.1)
     used = {t.data_ptr() for t in (*QUERY, lc.rows, idx, out, lse, lc.ws_sparse)}
     assert made == [(None, used), "left"]
+
+
+def kernel_rule(lens, n, counts, L):
+    """Lengths behind an append by misa_append_kv's rule, one sequence at a time."""
+    out = []
+    for b, l in enumerate(lens):
+        c = n if counts is None else counts[b]
+        out.append(l + c if 0 <= c <= n and l >= 0 and l + c <= L else l)
+    return out
+
+
+@pytest.mark.parametrize("n", [1, 3, 16, 17])
+def test_lengths_advance_where_rows_were_written(calls, monkeypatch, n):
+    """For every length and count at the borders, those out of range included."""
+    monkeypatch.setattr(latent, "append_kv", lambda *a, **kw: None)
+    top = 2 ** 31 - 1
+    lens = [-top - 1, -n, -1, 0, 1, 16 - n, 17 - n, 15, 16, 17, top - 1, top]
+    for counts in (None, -top - 1, -1, 0, 1, n - 1, n, n + 1, 16, top):
+        lc = cache("mx8", nseq=len(lens))
+        lc.lens.copy_(torch.tensor(lens, dtype=i32))
+        each = None if counts is None else [counts] * len(lens)
+        lc.append(torch.zeros(len(lens), n, 576, dtype=bf), counts=None if each is None else torch.tensor(each, dtype=i32))
+        assert lc.lens.tolist() == kernel_rule(lens, n, each, 16), counts
