@@ -218,6 +218,8 @@ class LatentCache:
         self.nseq, self.L, self.form, self.T, self.Hq, self.k = nseq, L, form, T, Hq, k
         self.rows = alloc_kv_cache(nseq, L, form, device)
         self.lens = torch.zeros(nseq, dtype=torch.int32, device=device)
+        self._new_lens = torch.empty_like(self.lens)    # append's temporaries
+        self._fits, self._also = (torch.empty(nseq, dtype=torch.bool, device=device) for _ in range(2))
         self._listed, self._prefix = ((torch.empty((T, Hq, MLA_DV), dtype=torch.bfloat16, device=device),
                                        torch.empty((T, Hq), dtype=torch.float32, device=device)) for _ in range(2))
         self.out, self.lse = self._listed
@@ -232,12 +234,19 @@ class LatentCache:
         is left as it was, as misa_append_kv skips it and records it in `ws`."""
         append_kv(self.rows, self.lens, rows, counts=counts, workspace=self.ws)
         n = rows.shape[1]
-        more = n if counts is None else counts
-        new = self.lens + more
-        fits = (new <= self.L) & (new >= more)   # (a length below zero, or past 2^31, gives less)
-        if counts is not None:
-            fits &= (counts >= 0) & (counts <= n)
-        self.lens.copy_(torch.where(fits, new, self.lens))
+        lens, new, fits, also = self.lens, self._new_lens, self._fits, self._also
+        if counts is None:
+            if n <= self.L:
+                torch.clamp(lens, 0, self.L - n, out=new)
+                torch.eq(new, lens, out=fits)
+                lens.add_(fits, alpha=n)
+            return
+        torch.clamp(counts, 0, n, out=new)
+        torch.eq(new, counts, out=fits)
+        torch.add(lens, counts, out=new)
+        fits.logical_and_(torch.le(new, self.L, out=also))
+        fits.logical_and_(torch.ge(new, counts, out=also))   # (a length below zero, or past 2^31, gives less)
+        torch.where(fits, new, lens, out=lens)
 
     def attend(self, q, seq_of, idx, scale: float):
         """Over the tokens the indexer lists -> (out, lse)."""

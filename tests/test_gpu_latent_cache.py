@@ -82,3 +82,23 @@ def test_lengths_and_rows_advance_together(counted):
     lc.append(rows.cuda(), counts=_i32(counts) if counted else None)
     assert lc.lens.tolist() == new and torch.equal(lc.rows.cpu(), want)
     assert misa.error_query(lc.ws) == misa._native.DEVERR_BAD_LEN
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_step_allocates_nothing(form):
+    T, L, k, Hq = 2, 64, 8, 16
+    lc = misa.LatentCache(T, L, form, T, Hq, k)
+    rows, q = torch.randn(T, 3, 576, device="cuda").bfloat16(), torch.randn(T, Hq, 576, device="cuda").bfloat16()
+    counts, seq, idx = _i32([2, 3]), _i32([0, 1]), _i32([[0, 1, -1, -1, -1, -1, -1, -1]] * T)
+
+    def step():
+        lc.append(rows)
+        lc.append(rows, counts=counts)
+        lc.attend(q, seq, idx, SCALE)
+        lc.attend_prefix(q, seq, lc.lens, SCALE)
+
+    step()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    step()
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    assert lc.lens.tolist() == [10, 12]

@@ -4,6 +4,7 @@ import contextlib
 
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import sparse_attention_token_misa_b200 as misa
 from sparse_attention_token_misa_b200 import _native as nat
@@ -96,3 +97,28 @@ def test_lengths_advance_where_rows_were_written(calls, monkeypatch, n):
         each = None if counts is None else [counts] * len(lens)
         lc.append(torch.zeros(len(lens), n, 576, dtype=bf), counts=None if each is None else torch.tensor(each, dtype=i32))
         assert lc.lens.tolist() == kernel_rule(lens, n, each, 16), counts
+
+
+class Fresh(TorchDispatchMode):
+    """Counts operations whose result stands in memory that none of their arguments had."""
+
+    def __init__(self):
+        super().__init__()
+        self.made = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        given = {t.untyped_storage().data_ptr() for t in (*args, *(kwargs or {}).values()) if isinstance(t, torch.Tensor)}
+        if isinstance(out, torch.Tensor) and out.untyped_storage().data_ptr() not in given:
+            self.made.append(str(func))
+        return out
+
+
+@pytest.mark.parametrize("n", [0, 1, 3, 17])
+def test_append_makes_no_tensors(calls, monkeypatch, n):
+    monkeypatch.setattr(latent, "append_kv", lambda *a, **kw: None)
+    lc, rows = cache("mx8", nseq=4), torch.zeros(4, n, 576, dtype=bf)
+    for counts in (None, torch.tensor([0, 1, n, 2], dtype=i32)):
+        with Fresh() as f:
+            lc.append(rows, counts=counts)
+        assert f.made == []
