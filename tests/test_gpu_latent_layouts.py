@@ -123,3 +123,56 @@ def test_a_listed_cache_gives_what_the_prefix_does(form, T, L):
     for out, lse in (misa.prefix_mla(q.cuda(), cache, _i32(seq), _i32([100] * T), SCALE, want_lse=True),
                      misa.sparse_mla_q(q.cuda(), cache, _i32(seq), _i32(every), SCALE, want_lse=True)):
         _check(out, lse, q, held, seq, _prefix_idx([100] * T, L), SCALE)
+
+
+@pytest.mark.parametrize("form", ["mx8", "mx4"])
+def test_longest_lists(form):
+    T, L, k = 2, 20000, 16384
+    q, cache, held = _setup(64, 1, L, form, T, 128)
+    idx = _draw_idx(64, T, L, k, 0)
+    idx[1, 5:16000] = -1
+    out, lse = misa.sparse_mla_q(q.cuda(), cache, _i32([0, 0]), _i32(idx), SCALE, want_lse=True)
+    _check(out, lse, q, held, np.zeros(T, np.int64), idx, SCALE)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_very_many_queries(form):
+    """Hundreds of items a cluster, a third of them without rows, one head each."""
+    T, L = 30000, 90
+    q, cache, held = _setup(65, 2, L, form, T, 1)
+    rng = np.random.default_rng(65)
+    lens = np.where(rng.random(T) < 0.3, 0, rng.integers(1, L + 1, T))
+    lens[200:4000] = 0
+    seq = rng.integers(0, 2, T)
+    out, lse = misa.prefix_mla(q.cuda(), cache, _i32(seq), _i32(lens), SCALE, want_lse=True)
+    _check(out, lse, q, held, seq, _prefix_idx(lens, L), SCALE)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_captured_with_everything_left_to_the_call(form):
+    """Outputs and workspace allocated inside the capture; replayed on new inputs."""
+    T, L = 3, 2100
+    q, cache, held = _setup(66, 2, L, form, T, 128)
+    qd, lens, seq, kept = torch.zeros(T, 128, 576, dtype=torch.bfloat16, device="cuda"), _i32([L, 5, 900]), _i32([0, 1, 0]), []
+    graph = misa.indexer.capture_graph(lambda: kept.append(misa.prefix_mla(qd, cache, seq, lens, SCALE, want_lse=True)))
+    out, lse = kept[-1]
+    for _ in range(2):
+        q = q.flip(0).contiguous()
+        qd.copy_(q)
+        graph.replay()
+        _check(out, lse, q, held, np.array([0, 1, 0]), _prefix_idx([L, 5, 900], L), SCALE)
+
+
+@pytest.mark.parametrize("form", ["mx8", "mx4"])
+def test_listed_calls_at_once(form):
+    """Rows split over clusters on two streams, with a workspace each: the same bits as alone."""
+    q, cache, _ = _setup(67, 2, 3000, form, 4, 128)
+    sets = [(q.cuda(), cache, _i32([0, 1, 0, 1]), _i32(_draw_idx(s, 4, 3000, 2048, 100 * s)), SCALE) for s in (0, 1)]
+    alone = [misa.sparse_mla_q(*x, want_lse=True) for x in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        both = [misa.sparse_mla_q(*x, want_lse=True, stream=s) for x, s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for one, other in zip(alone, both):
+            assert torch.equal(one[0], other[0]) and torch.equal(one[1], other[1])
