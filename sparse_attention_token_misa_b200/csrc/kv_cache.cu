@@ -1,14 +1,15 @@
 // The latent cache written and read back (include/misa_latent.h).
 //
 // Both kernels are one pass over the rows and bound by HBM, if few enough
-// instructions go into a row.  A warp takes several rows, four at a time: its lanes
+// instructions go into a row (writing mx4 takes 0.70 of the issue slots, reading 0.39).  A warp takes several rows, four at a time: its lanes
 // first find a row each (its sequence, its place in the cache), then all lanes take
 // each of the four rows' 64 pieces of eight latent entries, two pieces a lane, and
 // the 4 x 8 rotary pieces once.  The four pieces that share a scale are four
 // neighbouring lanes.  (A thread that found its own piece's row spent more on that
 // than on the piece: 65,536 rows of mx4 took 35 us to read.)  Measured, 65,536 rows
 // with the cache not in L2: mx8 118 MB read in 20.5 us (5.8 TB/s), listed rows 22.6,
-// written 22.6; mx4 102 MB 18.4, 20.5 and 22.5; bf16 151 MB 24.6 (a plain copy: 24.5).
+// written 22.6; mx4 102 MB 18.4, 20.5 and 22.5; bf16 151 MB 24.6 (a plain copy:
+// 22.5 to 24.5).
 #include "kv_format.cuh"
 #include "launch.h"
 #include "misa_device.cuh"

@@ -32,17 +32,18 @@
 // S 36 x 24 cycles (queries and rows, 3 KB at 128 bytes a cycle), O 4 x 2 x 48, and
 // rows and values written (bf16: and copied) once more, about 2000 cycles in all.
 // Measured, 74 queries of one cache, for 128 rows of it: bf16 2.1 us (1.26 PFLOP/s,
-// 0.79 of cuBLAS's measured rate), mx8 2.5, mx4 2.4, where the eight warps that widen
-// rows take longer than that.  More of them were slower (16: mx8 2.9), and so were
+// 0.76 of cuBLAS's measured rate in a burst, 0.90 of its sustained one), mx8 2.5 to
+// 2.7, mx4 2.4 to 2.7, where the eight warps that widen rows take longer than that.  More of them were slower (16: mx8 2.9), and so were
 // spilled registers: shared memory leaves L1 little room for a stack.
 //
 // A cluster stays on its SMs and takes one item in 74 (a query, or a part of its
 // rows), each role on its own: the rows of the next item come while the output of
 // this one leaves.  (A cluster an item spent 9 us on starting, queries and output
-// around 3 us a tile; now an item costs 4.)  Few queries: the rows of each are split
+// around 3 us a tile; now an item costs 3 to 4 besides its tiles.)  Few queries: the rows of each are split
 // over several items, whose partial sums a second kernel joins in a fixed order.
 //
-// Roles (640 threads a CTA): two warpgroups softmax and output, eight warps that bring
+// Roles (640 threads a CTA): two warpgroups softmax and output (what they tell one
+// another, and in what order, is in softmax_exchange.h), eight warps that bring
 // quantised rows or copy bf16 ones, one warp that has TMEM and, in the first CTA,
 // issues S, one that issues O, and two that ask for what comes by TMA and pass on what
 // has landed.  Shared memory is addressed from one 32-bit base: with a pointer a
@@ -1056,14 +1057,20 @@ latent_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
   if (lse && e4 == 0) lse[row] = any ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
 }
 
-// Clusters that run at once on the 148 SMs of a B200.
+// Clusters that run at once on the 148 SMs of a B200.  No cluster waits for another, so
+// a device with fewer SMs would only run them in turn.
 constexpr int kSlots = 74;
 
 // How many items share a query's rows: the split that makes the busiest cluster's list
-// shortest, counted in tiles.  An item more costs a cluster about as much as 16 tiles
-// (its queries, its output, and waiting for both), a join 6.  Measured: 64 queries of
-// 2048 mx8 rows 51 us whole and 69 in halves, 32 queries 49 and 40; 16 of 32,768 rows
-// 177 us in four parts and 187 in nine.
+// shortest, counted in tiles (1.1 to 1.35 us).  The constants fit whole calls, not their
+// parts: an item more in a cluster's list takes 3 to 4 us, but a part of a query also
+// writes fp32 sums (256 KB at 128 heads) that the join reads again, and the 16 tiles an
+// item stand for that too.  Measured, rows in L2: 64 queries of 2048 mx8 rows 50.5 us
+// whole and 65.2 in halves; 32 queries 48.5 whole, 34.9 in halves, 47.2 in thirds; 16 of
+// 32,768 rows 174 in four parts, 278 in five, 173 in nine.
+// n is the room for rows (k, or L): lengths are on the device.  A cache with far more
+// room than rows is split too often: 32 queries of 2048 mx8 rows take 35 us with room for
+// up to 32,768 rows and 70 with room for 131,072 (nine parts each).
 constexpr int kItemTiles = 16, kJoinTiles = 6;
 constexpr int kMaxParts = 4 * kSlots;   // of all queries together
 int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
