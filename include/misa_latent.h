@@ -97,12 +97,14 @@ MISA_API misa_status misa_read_kv(const void* cache, int fmt, int64_t nseq, int6
  *   idx_stride >= k) in cache seq_of[t]; -1 = empty slot, others outside [0, L)
  *   are treated as empty and set MISA_DEVERR_BAD_INDEX.  A token listed twice
  *   counts twice.  out: [T][Hq][512] bf16.  lse: [T][Hq] fp32, may be NULL.
- * A query with no valid slot, or with seq_of[t] outside [0, nseq) (which sets
- *   MISA_DEVERR_BAD_SEQ), gets zeros and lse = -inf.
+ * A query with no valid slot, with scores of -inf only, or with seq_of[t] outside
+ *   [0, nseq) (which sets MISA_DEVERR_BAD_SEQ), gets zeros and lse = -inf.  A NaN
+ *   or +inf among the scores gives NaN.
  * Precision: products of bf16 numbers summed in fp32; weights summed in fp32 and
  *   rounded to bf16 for the value product; one rounding to bf16 at the end.
  * Limits: 1 <= Hq <= 128, 1 <= k <= MISA_MAX_TOPK, T, L, nseq >= 1, L < 2^31,
- *   T * Hq < 2^31, T < 2^29; scale finite and >= 0; q, cache, out 16-byte aligned;
+ *   T * Hq < 2^31, T < 2^29; scale finite and >= 0, and so scale * log2(e) in
+ *   fp32; q, cache, out 16-byte aligned;
  *   cache_seq_stride as misa_read_kv; fmt MISA_KV_MX8 or MISA_KV_MX4
  *   (misa_sparse_mla reads bf16 rows).
  * workspace: >= misa_workspace_bytes(MISA_OP_SPARSE_MLA_Q, T, Hq, 0, 0, k, 0).

@@ -35,6 +35,8 @@ misa_status attend(misa::LatentArgs& a, int64_t n, float scale, void* ws, size_t
   misa_status st = check_cache(a.cache, a.fmt, a.nseq, a.seq_stride, a.L);
   if (st != MISA_OK) return st;
   if (!aligned16(a.q) || !aligned16(a.out)) return MISA_ERR_INVALID_ARG;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(a.scale_log2)) return MISA_ERR_UNSUPPORTED;   // infinity times a score of 0 would be NaN
   if (a.Hq > MISA_MAX_HEADS || static_cast<int64_t>(a.T) * a.Hq >= kMax31 || a.T >= (1 << 29))
     return MISA_ERR_UNSUPPORTED;
   // a TMA map reads bf16 rows: its strides are 40 bits
@@ -42,7 +44,6 @@ misa_status attend(misa::LatentArgs& a, int64_t n, float scale, void* ws, size_t
     return MISA_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, kErrBytes + misa::latent_mla_scratch_bytes(a.T, a.Hq, n));
   if (st != MISA_OK) return st;
-  a.scale_log2 = scale * 1.4426950408889634f;
   a.err = static_cast<uint32_t*>(ws);
   a.scratch = static_cast<uint8_t*>(ws) + kErrBytes;
   return cuda_status(misa::launch_latent_mla(a, reinterpret_cast<cudaStream_t>(stream)));

@@ -74,3 +74,27 @@ def test_scale_of_zero_keeps_nan_and_infinities(form):
     out, lse = misa.prefix_mla(q.cuda(), cache, _i32([0, 0]), _i32([70, 71]), 0.0, want_lse=True)
     assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
     _check(out[:1], lse[:1], q[:1], held[:, :70], np.zeros(1, np.int64), _prefix_idx([70], 70), 0.0)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("L", [70, 3000])
+def test_scores_that_are_not_finite(form, L):
+    """-inf has no weight, alone it is a query without rows; +inf gives NaN.  In one
+    part and in several."""
+    g = torch.Generator().manual_seed(52)
+    q = torch.randn(4, 128, 576, generator=g).bfloat16()
+    rows = torch.randn(4, L, 576, generator=g).bfloat16()
+    q[:, :, 570] = 1.0
+    rows[0, :, 570] = -float("inf")
+    rows[1, :, 570] = -float("inf")
+    rows[1, 65:68, 570] = 0.5
+    rows[2, 3, 570] = float("inf")
+    cache = misa.alloc_kv_cache(4, L, form)
+    misa.append_kv(cache, _i32([0] * 4), rows.cuda())
+    held = oracle.latent_values(rows.double().numpy(), form)
+    out, lse = misa.prefix_mla(q.cuda(), cache, _i32([0, 1, 2, 3]), _i32([L] * 4), SCALE, want_lse=True)
+    assert not out[0].any() and torch.isneginf(lse[0]).all()
+    assert torch.isnan(out[2]).all() and torch.isnan(lse[2]).all()
+    keep = np.full((2, L), -1)
+    keep[0, :3], keep[1] = [65, 66, 67], np.arange(L)
+    _check(out[[1, 3]], lse[[1, 3]], q[[1, 3]], held, np.array([1, 3]), keep, SCALE)

@@ -1,5 +1,7 @@
-"""Workspaces of the latent attention: one sized for a batch serves every smaller
-call (fewer queries, heads, listed tokens or rows), and its size is a formula."""
+"""Limits of the latent attention.  Workspaces: one sized for a batch serves every
+smaller call (fewer queries, heads, listed tokens or rows), and its size is a formula.
+Scales: those whose product with log2(e) fp32 does not hold are refused (the addresses
+below are never touched)."""
 import pytest
 
 import sparse_attention_token_misa_b200 as misa
@@ -44,3 +46,13 @@ def test_formula(op):
             parts = [t * min(128, -(-n // 64), 296 // t) for t in range(1, min(T, 148) + 1)
                      if min(128, -(-n // 64), 296 // t) > 1]
             assert size(op, T, 96, n) == 256 + max(parts, default=0) * 96 * 514 * 4, (T, n)
+
+
+P = 1 << 20
+
+
+@pytest.mark.parametrize("scale", [2.36e38, 3.4e38])
+def test_scales_too_large_are_refused(scale):
+    tail = (scale, P, None, P, 1 << 40, None)
+    assert misa.lib().misa_sparse_mla_q(P, P, 1, 2, 6560, 10, P, 2, 128, P, 8, 8, *tail) == 2     # unsupported
+    assert misa.lib().misa_prefix_mla(P, P, 1, 2, 6560, 10, P, P, 2, 128, *tail) == 2
