@@ -165,7 +165,7 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
 // Waits until the phase of `parity` is over; gives up after about two seconds
 // (counted in cycles: the nanosecond timer is read through the pipe that the
 // softmax's exponentials need).
-constexpr uint32_t kWaitCycles = 3900000000u;
+constexpr uint32_t kWaitCycles = 3900000000u, kDrainCycles = 20000000u;
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint32_t* err) {
   if (try_phase(bar, parity)) return true;
   const uint32_t t0 = clock();
@@ -178,7 +178,7 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, uint32_t
 }
 // The wait at the end of a cluster's work, which may take as long as all of it: its
 // limit counts from the last time that O went on.
-__device__ __forceinline__ void wait_all(uint32_t sb, uint32_t* err) {
+__device__ __forceinline__ bool wait_all(uint32_t sb, uint32_t* err) {
   uint32_t t0 = clock();
   bool seen = try_phase(sb + kPvDone, 0);
   while (!try_phase(sb + kDone, 0)) {
@@ -187,9 +187,10 @@ __device__ __forceinline__ void wait_all(uint32_t sb, uint32_t* err) {
     seen = now;
     if (static_cast<uint32_t>(clock()) - t0 > kWaitCycles) {
       record_error(err, MISA_DEVERR_TIMEOUT);
-      return;
+      return false;
     }
   }
+  return true;
 }
 // A wait of a whole warp: one outcome for all lanes.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t* err) {
@@ -390,7 +391,7 @@ struct Turn {
 // registers are free: behind the first writes they came late (mx8, 16 x 32,768 rows:
 // 178 and 192 us).
 template <int kFmt>
-__device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
+__device__ __forceinline__ bool bring_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
   const int r0 = tid >> 3, piece = tid & 7, own = static_cast<int>(rank) * kRows + r0;
   const uint32_t turn = (piece ^ (r0 & 7)) << 4;
@@ -431,7 +432,7 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, in
       }
       const uint4 y8 = rope;
       load(tile + 1);
-      if (!wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return;
+      if (!wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return false;
       const uint32_t kdst = kdst0 + n.stage() * kKStage;
 #pragma unroll
       for (int b = 0; b < 8; ++b) st_shared16(kdst + b * kKBlock, y[b]);
@@ -439,7 +440,7 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, in
       fence_proxy_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) arrive_in(sb + kKFull + n.at(), 0);
-      if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return;
+      if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return false;
       const uint32_t vofs = n.stage() * kVStage, far_bar = far_bar0 + n.at();
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
@@ -451,11 +452,12 @@ __device__ __forceinline__ void bring_rows(const MlaParams& p, uint32_t rank, in
       if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + n.at(), 0);
     }
   }
+  return true;
 }
 
 // Copies this CTA's rows of a bf16 cache, 256 threads as above, to O's operand.
 // Absent rows are cleared: P is 0 there, but 0 times a stale NaN is not.
-__device__ __forceinline__ void copy_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
+__device__ __forceinline__ bool copy_rows(const MlaParams& p, uint32_t rank, int tid, uint32_t sb) {
   const int r0 = tid >> 3, piece = tid & 7, own = static_cast<int>(rank) * kRows + r0;
   const uint32_t turn = (piece ^ (r0 & 7)) << 4;
   const uint32_t src0 = sb + kOffK + r0 * 128 + turn, vdst0 = sb + kOffV + own * 128 + turn;
@@ -464,7 +466,7 @@ __device__ __forceinline__ void copy_rows(const MlaParams& p, uint32_t rank, int
   for (Items it(p); it.next(p);)
 #pragma unroll 1
     for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
-      if (!wait_warp(sb + kKHere + n.at(), n.parity(), p.a.err)) return;
+      if (!wait_warp(sb + kKHere + n.at(), n.parity(), p.a.err)) return false;
       uint4 y[8];
 #pragma unroll
       for (int b = 0; b < 8; ++b) y[b] = ld_shared16(src0 + n.stage() * kKStage + b * kKBlock);
@@ -475,7 +477,7 @@ __device__ __forceinline__ void copy_rows(const MlaParams& p, uint32_t rank, int
       fence_proxy_async_smem();   // read before TMA may write there again
       __syncwarp();
       if ((threadIdx.x & 31) == 0) arrive_here(sb + kCopied + n.at());
-      if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return;
+      if (!wait_warp(sb + kVEmpty + n.at(), n.before(), p.a.err)) return false;
       const uint32_t vofs = n.stage() * kVStage;
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
@@ -486,10 +488,11 @@ __device__ __forceinline__ void copy_rows(const MlaParams& p, uint32_t rank, int
       __syncwarp();
       if ((threadIdx.x & 31) == 0) arrive_in(sb + kVFull + n.at(), 0);
     }
+  return true;
 }
 
 // Passes on to the first CTA what the other one has written here, a warp.
-__device__ __forceinline__ void pass_values(const MlaParams& p, int lane, uint32_t sb) {
+__device__ __forceinline__ bool pass_values(const MlaParams& p, int lane, uint32_t sb) {
   if (lane == 0) {
     bar_expect(sb + kVLanded, kVStage / 2);
     bar_expect(sb + kVLanded + 8, kVStage / 2);
@@ -498,13 +501,14 @@ __device__ __forceinline__ void pass_values(const MlaParams& p, int lane, uint32
   for (Items it(p); it.next(p);)
 #pragma unroll 1
     for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
-      if (!wait_warp(sb + kVLanded + n.at(), n.parity(), p.a.err)) return;
+      if (!wait_warp(sb + kVLanded + n.at(), n.parity(), p.a.err)) return false;
       if (lane == 0) {
         bar_expect(sb + kVLanded + n.at(), kVStage / 2);   // for the tile after the next
         asm volatile("fence.proxy.async;" ::: "memory");
         arrive_in(sb + kVFull + n.at(), 0);
       }
     }
+  return true;
 }
 
 // Brings the queries of this CTA's heads, and asks the quantised rows of tiles ahead
@@ -517,21 +521,21 @@ __device__ __forceinline__ void load_queries(const MlaParams& p, uint32_t rank, 
 }
 constexpr int kAhead = 4;   // tiles (2, 8 and 12: the same within 3 %)
 template <int kFmt>
-__device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, int lane, const CUtensorMap* q_map, uint32_t sb) {
+__device__ __forceinline__ bool look_ahead(const MlaParams& p, uint32_t rank, int lane, const CUtensorMap* q_map, uint32_t sb) {
   constexpr int kRow = kv_row_bytes(kFmt);
   uint32_t items = 0;
   Turn n;
   for (Items it(p); it.next(p); ++items) {
     const Work& w = it.w;
-    if (!wait_warp(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
+    if (!wait_warp(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return false;
     if (elect_one()) load_queries(p, rank, w.t, q_map, sb);
     __syncwarp();
-    if (!wait_warp(sb + kQFull, items & 1, p.a.err)) return;
+    if (!wait_warp(sb + kQFull, items & 1, p.a.err)) return false;
     if (lane == 0) arrive_in(sb + kQReady, 0);
     for (int tile = w.tile0; tile < w.tile1; ++tile, ++n.n) {
       // Goes on with the tiles: S of this one waits for the arrival, so that no phase
       // can pass by unseen.
-      if (!wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return;
+      if (!wait_warp(sb + kKEmpty + n.at(), n.before(), p.a.err)) return false;
       if (lane == 0) arrive_in(sb + kKFull + n.at(), 0);
       if (tile + kAhead >= w.tile1) continue;
       const int first = (tile + kAhead) * kTile + static_cast<int>(rank) * kRows;
@@ -549,17 +553,18 @@ __device__ __forceinline__ void look_ahead(const MlaParams& p, uint32_t rank, in
       for (int o = 0; o < kRow; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + o));
     }
   }
+  return true;
 }
 
 // Of a bf16 cache, brings queries and rows by TMA; one thread.
-__device__ __forceinline__ void ask_rows(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
+__device__ __forceinline__ bool ask_rows(const MlaParams& p, uint32_t rank, const CUtensorMap* q_map, const CUtensorMap* map, uint32_t sb) {
   uint32_t items = 0;
   Turn n;
   for (Items it(p); it.next(p); ++items) {
     for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
       const int row = tile * kTile + static_cast<int>(rank) * kRows;
       const uint32_t bar = sb + kKHere + n.at();
-      if (!wait_one(sb + kKEmpty + n.at(), n.before(), p.a.err) || !wait_one(sb + kCopied + n.at(), n.before(), p.a.err)) return;
+      if (!wait_one(sb + kKEmpty + n.at(), n.before(), p.a.err) || !wait_one(sb + kCopied + n.at(), n.before(), p.a.err)) return false;
       bar_expect(bar, kKStage);
 #pragma unroll 1
       for (int b = 0; b < kBlocks; ++b) {
@@ -567,25 +572,27 @@ __device__ __forceinline__ void ask_rows(const MlaParams& p, uint32_t rank, cons
         if (tile + kAhead < it.w.tile1) tma_l2_3d(map, b * 64, row + kAhead * kTile, it.w.seq);
       }
       if (tile == it.w.tile0) {   // the first rows need not wait for the place of the queries
-        if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return;
+        if (!wait_one(sb + kQEmpty, (items & 1) ^ 1u, p.a.err)) return false;
         load_queries(p, rank, it.w.t, q_map, sb);
       }
     }
   }
+  return true;
 }
 // Passes on to the first CTA what has landed in the second, one thread.
-__device__ __forceinline__ void pass_rows(const MlaParams& p, uint32_t sb) {
+__device__ __forceinline__ bool pass_rows(const MlaParams& p, uint32_t sb) {
   uint32_t items = 0;
   Turn n;
   for (Items it(p); it.next(p); ++items) {
-    if (!wait_one(sb + kQFull, items & 1, p.a.err)) return;
+    if (!wait_one(sb + kQFull, items & 1, p.a.err)) return false;
     arrive_in(sb + kQReady, 0);
 #pragma unroll 1
     for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
-      if (!wait_one(sb + kKHere + n.at(), n.parity(), p.a.err)) return;
+      if (!wait_one(sb + kKHere + n.at(), n.parity(), p.a.err)) return false;
       arrive_in(sb + kKFull + n.at(), 0);
     }
   }
+  return true;
 }
 
 // Issue the products of both CTAs, two warps of the first: S of one tile after the
@@ -593,12 +600,13 @@ __device__ __forceinline__ void pass_rows(const MlaParams& p, uint32_t sb) {
 // comes first.  (One warp for both had to look at six barriers in turn, at 50 to 90
 // cycles each: it saw an operand 300 to 800 cycles late.)  All lanes wait, one issues.
 template <bool kQuant>
-__device__ __forceinline__ void multiply_rows(const MlaParams& p, uint32_t tmem, uint32_t sb) {
+__device__ __forceinline__ bool multiply_rows(const MlaParams& p, uint32_t tmem, uint32_t sb) {
   const bool leader = elect_one();
+  bool ok = false;
   Turn n;
   uint32_t items = 0;
   for (Items it(p); it.next(p); ++items) {
-    if (!wait_warp(sb + kQReady, items & 1, p.a.err) || (!kQuant && !wait_warp(sb + kQFull, items & 1, p.a.err))) break;
+    if (!wait_warp(sb + kQReady, items & 1, p.a.err) || (!kQuant && !wait_warp(sb + kQFull, items & 1, p.a.err))) goto done;
 #pragma unroll 1
     for (int left = it.w.tile1 - it.w.tile0; left > 0; --left, ++n.n) {
       if (!wait_warp(sb + kSEmpty + n.at4(), n.parity4() ^ 1u, p.a.err) || !wait_warp(sb + kKFull + n.at(), n.parity(), p.a.err) ||
@@ -634,16 +642,19 @@ __device__ __forceinline__ void multiply_rows(const MlaParams& p, uint32_t tmem,
       __syncwarp();
     }
   }
+  ok = true;
 done:
   if (leader) commit_pair(sb + kDone);
   __syncwarp();
+  return ok;
 }
-__device__ __forceinline__ void multiply_values(const MlaParams& p, uint32_t tmem, uint32_t sb) {
+__device__ __forceinline__ bool multiply_values(const MlaParams& p, uint32_t tmem, uint32_t sb) {
   const bool leader = elect_one();
+  bool ok = false;
   Turn n;
   uint32_t items = 0;
   for (Items it(p); it.next(p); ++items) {
-    if (!wait_warp(sb + kOEmpty, (items & 1) ^ 1u, p.a.err)) break;
+    if (!wait_warp(sb + kOEmpty, (items & 1) ^ 1u, p.a.err)) goto done;
 #pragma unroll 1
     for (int tile = it.w.tile0; tile < it.w.tile1; ++tile, ++n.n) {
       if (!wait_warp(sb + kVFull + n.at(), n.parity(), p.a.err) || !wait_warp(sb + kPFull + n.at(), n.parity(), p.a.err)) goto done;
@@ -666,9 +677,11 @@ __device__ __forceinline__ void multiply_values(const MlaParams& p, uint32_t tme
       __syncwarp();
     }
   }
+  ok = true;
 done:
   if (leader) commit_pair(sb + kDone);
   __syncwarp();
+  return ok;
 }
 
 __device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
@@ -687,7 +700,7 @@ struct ExchangeIo {
 // loads, barriers and fences pass while the other one counts; between them goes the
 // reference m alone, early in a tile.  tid: in the warpgroup; its warp w has TMEM
 // lanes 32 w.., two lanes a head, one for each half of a tile's rows and of O.
-__device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint32_t group, int tid, uint32_t tmem, uint32_t sb) {
+__device__ __forceinline__ bool softmax(const MlaParams& p, uint32_t rank, uint32_t group, int tid, uint32_t tmem, uint32_t sb) {
   const LatentArgs& a = p.a;
   uint32_t* err = a.err;
   const int warp = tid >> 5, lane = tid & 31;
@@ -889,6 +902,7 @@ __device__ __forceinline__ void softmax(const MlaParams& p, uint32_t rank, uint3
     __syncwarp();
     if (lane == 0) arrive_in(sb + kOEmpty, 0);   // O has been read
   }
+  return ok;
 }
 
 template <int kFmt>
@@ -938,37 +952,43 @@ latent_mla_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
   pdl_wait_inputs();
   pdl_allow_next();
 
-  const LatentArgs& a = p.a;
-  uint32_t* err = a.err;
+  bool ok = true;
   if (warp == kMmaWarp) {
-    if (rank == 0) multiply_rows<kQuant>(p, tmem, sb);
-    wait_all(sb, err);   // nothing reads this CTA's memory any more
+    if (rank == 0) ok = multiply_rows<kQuant>(p, tmem, sb);
+    ok = wait_all(sb, p.a.err) && ok;   // nothing reads this CTA's memory any more
     __syncwarp();
   } else if (warp == kMmaWarp + 3) {
     if (rank == 0) {
-      multiply_values(p, tmem, sb);
+      ok = multiply_values(p, tmem, sb);
     } else if (!kQuant) {
-      if (elect_one()) pass_rows(p, sb);
+      if (elect_one()) ok = pass_rows(p, sb);
       __syncwarp();
     }
   } else if (warp == kMmaWarp + 1) {
-    pass_values(p, lane, sb);
+    ok = pass_values(p, lane, sb);
   } else if (warp == kMmaWarp + 2) {
     if constexpr (kQuant) {
-      look_ahead<kFmt>(p, rank, lane, &q_map, sb);
+      ok = look_ahead<kFmt>(p, rank, lane, &q_map, sb);
     } else {
-      if (elect_one()) ask_rows(p, rank, &q_map, &row_map, sb);
+      if (elect_one()) ok = ask_rows(p, rank, &q_map, &row_map, sb);
       __syncwarp();
     }
   } else if (warp >= kRowWarp0) {
-    if constexpr (kQuant) bring_rows<kFmt>(p, rank, tid - kRowWarp0 * 32, sb);
-    else copy_rows(p, rank, tid - kRowWarp0 * 32, sb);
+    if constexpr (kQuant) ok = bring_rows<kFmt>(p, rank, tid - kRowWarp0 * 32, sb);
+    else ok = copy_rows(p, rank, tid - kRowWarp0 * 32, sb);
   } else {
-    softmax(p, rank, warp >> 2, tid & 127, tmem, sb);
+    ok = softmax(p, rank, warp >> 2, tid & 127, tmem, sb);
   }
 
   tc_fence_before();
-  __syncthreads();
+  if (__syncthreads_or(!ok)) {
+    // A wait gave up: copies that a role had asked for (by TMA, or st.async to the other
+    // CTA) may be under way.  Neither CTA leaves before they have had some 10 ms to land;
+    // nothing waits for them by barrier, since one of those did not come.
+    const uint32_t t0 = clock();
+    while (static_cast<uint32_t>(clock()) - t0 < kDrainCycles) {
+    }
+  }
   cluster_sync_all();   // neither CTA leaves while the other may still arrive on its barriers
   tc_fence_after();
   if (warp == kMmaWarp)
